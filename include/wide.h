@@ -59,6 +59,7 @@ extern "C" {
 #define WIDE_DEV_TIMEOUT 0x2  /* a bounded wait inside a kernel gave up */
 #define WIDE_DEV_BAD_ITEM 0x4 /* a work-list entry was out of range */
 #define WIDE_DEV_LAYOUT 0x8   /* a kernel's shared-memory alignment precondition failed */
+#define WIDE_DEV_BAD_RANGE 0x10 /* a sequence's length, count or cache position was out of range */
 
 /* element types */
 #define WIDE_BF16 0
@@ -452,6 +453,154 @@ typedef struct wide_router_dims {
 
 int wide_route(const void *d_x, const void *d_w_r1, const void *d_w_r2, const float *d_b_r2,
                uint32_t *d_mask, float *d_logits, const wide_router_dims *d, void *stream);
+
+/* -------------------------------------------------------- rotary positions
+ *
+ * The rotation that wide_layer_masked applies inside its projections (half
+ * layout, whole head, unscaled), as a call of its own and in the other forms
+ * checkpoints use.  For every token t, head h and pair i of the first rot_dim
+ * elements, with the pair's elements a and b and A = amplitude,
+ *     angle = position[t] * f_i
+ *     out_a = A * (x_a cos(angle) - x_b sin(angle))
+ *     out_b = A * (x_b cos(angle) + x_a sin(angle))
+ * Elements from rot_dim on are copied.  Pairs: WIDE_ROPE_HALF
+ * (i, i + rot_dim / 2), WIDE_ROPE_INTERLEAVED (2 i, 2 i + 1).  Frequencies:
+ * f_i = theta^(-2 i / rot_dim), then, for a context `factor` times as long,
+ *     factor == 1            unscaled
+ *     original_len == 0      f_i / factor                        (linear)
+ *     else                   f_i * (g + (1 - g) / factor)        (ramp)
+ *         with g = clamp((r - low_freq) / (high_freq - low_freq), 0, 1) and
+ *         r = original_len * f_i / (2 pi), the turns a pair makes within the
+ *         original context: fast pairs keep their frequency.
+ * The rotation by -position undoes it (A = 1), and with any A it is the
+ * gradient: dx = wide_rope(d_out, -position).
+ * Frequencies and angles are computed in double (the host computes the
+ * frequencies of a call), reduced to one turn, then cos and sin in fp32;
+ * products and sums are fp32, rounded once to the element type.
+ */
+#define WIDE_ROPE_HALF 0
+#define WIDE_ROPE_INTERLEAVED 1
+typedef struct wide_rope_config {
+    int32_t rot_dim;       /* elements rotated: even, 2 .. 256 */
+    int32_t layout;        /* WIDE_ROPE_HALF or WIDE_ROPE_INTERLEAVED */
+    double theta;          /* base, > 0 */
+    double factor;         /* > 0 */
+    double low_freq, high_freq;   /* ramp: turns, 0 <= low_freq < high_freq */
+    int64_t original_len;  /* ramp: the original context, >= 0 */
+    double amplitude;      /* A, > 0 */
+} wide_rope_config;
+
+typedef struct wide_rope_dims {
+    int64_t tokens;
+    int32_t heads, head_dim;
+    int32_t dtype;                          /* WIDE_BF16 or WIDE_F32 */
+    int64_t x_token_stride, x_head_stride;  /* in elements; a row's elements are contiguous */
+    int64_t out_token_stride, out_head_stride;
+} wide_rope_dims;
+
+/* d_positions: int32 [tokens], any value.  d_out may be d_x itself with the
+ * same strides (in place); other overlaps are not allowed.  Any alignment and
+ * stride (strides of d_x >= 0; rows of d_out must not overlap); rows whose
+ * addresses, head_dim and rotated part are multiples of 16 bytes take the
+ * 16-byte path.  tokens == 0 enqueues nothing; head_dim even,
+ * <= 1024; heads * head_dim <= 2^20. */
+int wide_rope(const void *d_x, const int32_t *d_positions, void *d_out, const wide_rope_dims *d,
+              const wide_rope_config *rope, void *stream);
+
+/* --------------------------------------------------------------- KV cache
+ *
+ * The cache of wide_layer_masked, [n_seq][n_kv][cap][head_dim], in bf16 or in
+ * 8 bits.  An 8-bit cache holds one code per element and one scale per 32
+ * elements of a row, uint8 [n_seq][n_kv][cap][head_dim / 32]: a scale byte b
+ * stands for 2^(b - 127), and an element's value is code * 2^(b - 127).
+ *     WIDE_KV_E4M3   codes are e4m3 numbers, largest 448
+ *     WIDE_KV_I8     codes are two's complement, -127 .. 127
+ * Written: the scale is the smallest power of two s >= 2^-124 with
+ * max|x| <= 448 s (127 s), the code is x / s rounded to nearest, ties to
+ * even; a block of zeros has b = 0; a block that holds an infinity or a NaN
+ * has b = 255 and zero codes, and reads back as NaN.  Powers of two make the
+ * division and every value exact: what wide_kv_read returns in bf16, and what
+ * the attention multiplies, is the cached value itself.
+ */
+#define WIDE_KV_BF16 0
+#define WIDE_KV_E4M3 1
+#define WIDE_KV_I8 2
+typedef struct wide_kv_cache {
+    void *k, *v;                   /* device, 16-byte aligned */
+    uint8_t *k_scale, *v_scale;    /* device, 4-byte aligned; unused (NULL) for WIDE_KV_BF16 */
+    int64_t n_seq, cap;
+    int32_t n_kv, head_dim;        /* head_dim 128 */
+    int32_t kind;                  /* WIDE_KV_* */
+} wide_kv_cache;
+
+typedef struct wide_kv_rows {
+    int64_t seq_len;               /* token slots per sequence; token t = s * seq_len + i */
+    int64_t k_token_stride, k_head_stride;   /* of the bf16 rows, in elements (multiples of 8) */
+    int64_t v_token_stride, v_head_stride;
+} wide_kv_rows;
+
+/* Writes rows d_k, d_v (bf16 [n_seq * seq_len][n_kv][head_dim], strided) into
+ * the cache: token i < count[s] of sequence s goes to position start[s] + i;
+ * other tokens are neither read nor written.  d_start, d_count: int32
+ * [n_seq] (NULL: all 0, all seq_len).  rope (NULL: none): K is rotated in
+ * fp32 before it is rounded, by d_positions[t] (int32; NULL: its cache
+ * position); rot_dim <= 128 and, in the half layout, a multiple of 16.  V is
+ * never rotated.  A count outside 0 .. seq_len or a position outside
+ * 0 .. cap - 1 sets WIDE_DEV_BAD_RANGE; those rows are not written. */
+int wide_kv_append(const void *d_k, const void *d_v, const wide_kv_cache *cache,
+                   const int32_t *d_start, const int32_t *d_count, const int32_t *d_positions,
+                   const wide_kv_rows *rows, const wide_rope_config *rope, void *stream);
+
+/* The reverse: positions start[s] + i, i < count[s], of the cache into rows
+ * d_k, d_v (bf16, strided; exact).  Rows at or past count[s] are left as
+ * they were.  Errors as for wide_kv_append. */
+int wide_kv_read(void *d_k, void *d_v, const wide_kv_cache *cache, const int32_t *d_start,
+                 const int32_t *d_count, const wide_kv_rows *rows, void *stream);
+
+/* ------------------------------------------------- attention of draft trees
+ *
+ * The attention of several new tokens per sequence over the cache, skipping
+ * (token, head group) pairs as wide_attn_masked does: verification of a tree
+ * of drafted tokens, a chunk of a prompt, or single tokens of sequences of
+ * different lengths.  Sequence s has cache_len[s] earlier positions and
+ * draft_len[s] <= draft new tokens whose keys and values are in the cache
+ * already, at positions cache_len[s] + i (wide_kv_append).  New token i
+ * attends every earlier position and the new tokens j whose bit is set in
+ * its row of the tree mask: uint32 words [n_seq * draft][ceil(draft / 32)],
+ * bit j % 32 of word j / 32 (NULL: j <= i, a chain; bits at or past
+ * draft_len[s] are ignored).  For every kept pair of token t and head group,
+ * and each query head h of the group,
+ *     out[t][h] = sum_p softmax_p(scale * q[t][h] . k[p]) v[p]
+ * with scores, softmax and sums in fp32 and the weights rounded to bf16 for
+ * the product with v (as in the prefill layer).  A pair whose bit in
+ * d_head_mask ([n_seq * draft][ceil(n_kv / 32)]; NULL: all kept; bits at or
+ * past n_kv are ignored) is clear gets zeros, and so does a row that attends
+ * nothing.  Tokens at or past draft_len[s] are left as they were.  A cached value that
+ * is not finite reaches only the rows that attend its position.
+ *
+ * q: bf16 [n_seq * draft][n_q][128], tokens q_token_stride elements apart
+ * (a multiple of 8); out: bf16, contiguous.  d_cache_len, d_draft_len:
+ * int32 [n_seq] (draft_len NULL: all `draft`).  A sequence whose lengths are
+ * negative, draft_len > draft or cache_len + draft_len > cap sets
+ * WIDE_DEV_BAD_RANGE and is left out.
+ * Supported: head_dim 128; n_q a multiple of n_kv, n_q / n_kv <= 32; draft
+ * 1 .. 1024; n_seq * n_kv <= 4096.  The work is divided over the GPU on the
+ * device from the lengths and masks; results do not depend on timing.
+ * Workspace: >= wide_attn_tree_workspace_bytes, 256-byte aligned; contents
+ * need not be initialised; calls that share one must be ordered. */
+typedef struct wide_attn_tree_dims {
+    int64_t draft;           /* new-token slots per sequence */
+    int64_t q_token_stride;
+    int32_t n_q;
+    float scale;             /* > 0: multiplies q . k (1 / sqrt(128) as a rule) */
+} wide_attn_tree_dims;
+
+size_t wide_attn_tree_workspace_bytes(const wide_kv_cache *cache, const wide_attn_tree_dims *d);
+
+int wide_attn_tree(const void *d_q, const wide_kv_cache *cache, const int32_t *d_cache_len,
+                   const int32_t *d_draft_len, const uint32_t *d_tree_mask,
+                   const uint32_t *d_head_mask, void *d_out, const wide_attn_tree_dims *d,
+                   void *d_workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -14,9 +14,10 @@ Contents
   ffn.reorder           canonical mask reordering (C)
   attention.*           RMSNorm, RoPE, masked GQA attention, whole layer
   router.*              bottleneck router -> packed group masks (section 2.A)
+  serving.*             rotary positions, 8-bit cache rows, draft-tree attention
 
 Parity pins live in tests/test_oracle_*.py.  Nothing here is "parity
 unpinned".
 """
-from . import ffn, attention, router  # noqa: F401
+from . import ffn, attention, router, serving  # noqa: F401
 from ._clib import build  # noqa: F401

@@ -21,10 +21,12 @@ from . import _native
 from ._native import (  # noqa: F401
     WIDE_OK, WIDE_EINVAL, WIDE_EUNSUPPORTED, WIDE_EWORKSPACE, WIDE_ECUDA, WIDE_ETOOLARGE,
     WIDE_NOALLOC_SCRATCH_BYTES,
-    WIDE_DEV_BAD_MASK, WIDE_DEV_TIMEOUT, WIDE_DEV_BAD_ITEM, WIDE_DEV_LAYOUT,
+    WIDE_DEV_BAD_MASK, WIDE_DEV_TIMEOUT, WIDE_DEV_BAD_ITEM, WIDE_DEV_LAYOUT, WIDE_DEV_BAD_RANGE,
     WIDE_BF16, WIDE_F32, WIDE_PATH_AUTO, WIDE_PATH_DECODE, WIDE_PATH_PREFILL,
-    WIDE_ACT_RELU, WIDE_ACT_SILU,
+    WIDE_ACT_RELU, WIDE_ACT_SILU, WIDE_ROPE_HALF, WIDE_ROPE_INTERLEAVED,
+    WIDE_KV_BF16, WIDE_KV_E4M3, WIDE_KV_I8,
     WideWorklist, WideFFNDims, WideLayerDims, WideLayerWeights, WideRouterDims,
+    WideRopeConfig, WideRopeDims, WideKVCache, WideKVRows, WideAttnTreeDims,
 )
 
 _L = _native.lib()
@@ -478,3 +480,208 @@ def wide_route(x: torch.Tensor, w_r1: torch.Tensor, w_r2: torch.Tensor,
             None if logits is None else _dev_ptr(logits, "logits"), ctypes.byref(d),
             _stream(stream, dev)))
     return mask_words
+
+
+# -------------------------------------------------------- rotary positions
+
+def wide_rope_config(rot_dim: int, theta: float = 5e5, layout: int = WIDE_ROPE_HALF,
+                     factor: float = 1.0, low_freq: float = 0.0, high_freq: float = 0.0,
+                     original_len: int = 0, amplitude: float = 1.0) -> WideRopeConfig:
+    """The rotation's parameters.  ``factor`` stretches the context: linearly
+    with original_len 0, else frequency by frequency between low_freq and
+    high_freq turns of the original context."""
+    return WideRopeConfig(rot_dim, layout, theta, factor, low_freq, high_freq, original_len,
+                          amplitude)
+
+
+def _index(t, name: str, n: int, device):
+    """Device pointer of an int32 vector of n elements (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} must be int32 [{n}], got {t.dtype} {tuple(t.shape)}")
+    return _dev_ptr(t, name)
+
+
+def wide_rope(x: torch.Tensor, positions: torch.Tensor, rope: WideRopeConfig,
+              out: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """x (bf16 or fp32 [T][heads][head_dim], tokens and heads at any stride)
+    with the first rot_dim elements of every head rotated by the token's
+    position (int32 [T]).  ``out`` may be x."""
+    if x.dim() != 3:
+        raise ValueError(f"x must be [T][heads][head_dim], got {tuple(x.shape)}")
+    T, n, hd = x.shape
+    if out is None:
+        out = torch.empty((T, n, hd), dtype=x.dtype, device=x.device)
+    elif out.dtype != x.dtype or out.shape != x.shape:
+        raise ValueError(f"out must be {x.dtype} {tuple(x.shape)}")
+    if (x.stride(2) != 1 and hd > 1) or (out.stride(2) != 1 and hd > 1):
+        raise ValueError("the elements of a head must be contiguous")
+    dev = _one_device("wide_rope", x=x, positions=positions, out=out)
+    d = WideRopeDims(T, n, hd, _dtype_code(x), x.stride(0), x.stride(1), out.stride(0),
+                     out.stride(1))
+    pos = _index(positions, "positions", T, dev)
+    with torch.cuda.device(dev):
+        _check("wide_rope", _L.wide_rope(x.data_ptr(), pos, out.data_ptr(), ctypes.byref(d),
+                                         ctypes.byref(rope), _stream(stream, dev)))
+    return out
+
+
+# ---------------------------------------------------------------- KV cache
+
+_KV_KINDS = {torch.bfloat16: WIDE_KV_BF16, torch.float8_e4m3fn: WIDE_KV_E4M3,
+             torch.int8: WIDE_KV_I8}
+
+
+def wide_kv_cache(n_seq: int, n_kv: int, cap: int, dtype=torch.bfloat16, head_dim: int = 128,
+                  device="cuda") -> dict:
+    """A zeroed cache: k and v [n_seq][n_kv][cap][head_dim] of ``dtype`` (bf16,
+    float8_e4m3fn or int8) and, for the 8-bit types, k_scale and v_scale
+    uint8 [n_seq][n_kv][cap][head_dim / 32].  Any dict of such tensors is a
+    cache: {"k": k_cache, "v": v_cache} of wide_layer_masked, for one."""
+    if dtype not in _KV_KINDS:
+        raise TypeError(f"unsupported cache dtype {dtype}")
+    shape = (n_seq, n_kv, cap, head_dim)
+    cache = {n: torch.zeros(shape, dtype=dtype, device=device) for n in ("k", "v")}
+    if dtype != torch.bfloat16:
+        for n in ("k_scale", "v_scale"):
+            cache[n] = torch.zeros((n_seq, n_kv, cap, head_dim // 32), dtype=torch.uint8,
+                                   device=device)
+    return cache
+
+
+def _cache_tensors(cache: dict) -> dict:
+    return {"cache_" + n: cache.get(n) for n in ("k", "v", "k_scale", "v_scale")}
+
+
+def _kv_cache(cache: dict) -> WideKVCache:
+    k, v = cache["k"], cache["v"]
+    if k.dtype not in _KV_KINDS or v.dtype != k.dtype:
+        raise TypeError(f"unsupported cache dtypes {k.dtype}, {v.dtype}")
+    if k.dim() != 4 or v.shape != k.shape:
+        raise ValueError(f"cache k and v must be [n_seq][n_kv][cap][head_dim], got "
+                         f"{tuple(k.shape)}, {tuple(v.shape)}")
+    n_seq, n_kv, cap, hd = k.shape
+    ks = vs = None
+    if k.dtype != torch.bfloat16:
+        for n in ("k_scale", "v_scale"):
+            t = cache.get(n)
+            if t is None or t.dtype != torch.uint8 or \
+                    tuple(t.shape) != (n_seq, n_kv, cap, hd // 32):
+                raise ValueError(f"cache {n} must be uint8 [{n_seq}][{n_kv}][{cap}][{hd // 32}]")
+        ks, vs = _dev_ptr(cache["k_scale"], "k_scale"), _dev_ptr(cache["v_scale"], "v_scale")
+    return WideKVCache(_dev_ptr(k, "k"), _dev_ptr(v, "v"), ks, vs, n_seq, cap, n_kv, hd,
+                       _KV_KINDS[k.dtype])
+
+
+def _kv_rows(k, v, T: int, n_kv: int, hd: int, seq_len: int) -> WideKVRows:
+    for name, t in (("k", k), ("v", v)):
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, n_kv, hd):
+            raise ValueError(f"{name} must be bfloat16 [{T}][{n_kv}][{hd}], got {t.dtype} "
+                             f"{tuple(t.shape)}")
+        if t.stride(2) != 1:
+            raise ValueError(f"the elements of a head of {name} must be contiguous")
+    return WideKVRows(seq_len, k.stride(0), k.stride(1), v.stride(0), v.stride(1))
+
+
+def wide_kv_append(k: torch.Tensor, v: torch.Tensor, cache: dict, start: torch.Tensor = None,
+                   count: torch.Tensor = None, rope: WideRopeConfig = None,
+                   positions: torch.Tensor = None, stream=None) -> None:
+    """Writes k, v (bf16 [n_seq * seq_len][n_kv][head_dim], strided) into the
+    cache: token i < count[s] of sequence s at position start[s] + i (int32
+    [n_seq]; None: all 0, all seq_len).  ``rope`` rotates K on the way, by
+    ``positions`` (int32 [T]) or the cache positions."""
+    n_seq, n_kv, _, hd = cache["k"].shape
+    T = k.shape[0]
+    if n_seq == 0 or T % n_seq != 0:
+        raise ValueError(f"{T} rows do not divide into {n_seq} sequences")
+    rows = _kv_rows(k, v, T, n_kv, hd, T // n_seq)
+    dev = _one_device("wide_kv_append", k=k, v=v, start=start, count=count, positions=positions,
+                      **_cache_tensors(cache))
+    c = _kv_cache(cache)
+    st, ct = _index(start, "start", n_seq, dev), _index(count, "count", n_seq, dev)
+    ps = _index(positions, "positions", T, dev)
+    with torch.cuda.device(dev):
+        _check("wide_kv_append", _L.wide_kv_append(
+            k.data_ptr(), v.data_ptr(), ctypes.byref(c), st, ct, ps, ctypes.byref(rows),
+            None if rope is None else ctypes.byref(rope), _stream(stream, dev)))
+
+
+def wide_kv_read(cache: dict, start: torch.Tensor, seq_len: int, count: torch.Tensor = None,
+                 k: torch.Tensor = None, v: torch.Tensor = None, stream=None) -> tuple:
+    """(k, v) bf16 [n_seq * seq_len][n_kv][head_dim]: positions start[s] + i of
+    the cache, i < count[s] (None: 0 and seq_len).  Rows past count are left
+    as they were (zeros when k, v are not given)."""
+    n_seq, n_kv, _, hd = cache["k"].shape
+    T = n_seq * seq_len
+    make = torch.empty if count is None else torch.zeros
+    if k is None:
+        k = make((T, n_kv, hd), dtype=torch.bfloat16, device=cache["k"].device)
+    if v is None:
+        v = make((T, n_kv, hd), dtype=torch.bfloat16, device=cache["k"].device)
+    rows = _kv_rows(k, v, T, n_kv, hd, seq_len)
+    dev = _one_device("wide_kv_read", k=k, v=v, start=start, count=count,
+                      **_cache_tensors(cache))
+    c = _kv_cache(cache)
+    st, ct = _index(start, "start", n_seq, dev), _index(count, "count", n_seq, dev)
+    with torch.cuda.device(dev):
+        _check("wide_kv_read", _L.wide_kv_read(k.data_ptr(), v.data_ptr(), ctypes.byref(c), st, ct,
+                                               ctypes.byref(rows), _stream(stream, dev)))
+    return k, v
+
+
+# ------------------------------------------------ attention of draft trees
+
+def wide_attn_tree_workspace_bytes(cache: dict, draft: int, n_q: int) -> int:
+    c = _kv_cache(cache)
+    d = WideAttnTreeDims(draft, n_q * c.head_dim, n_q, 1.0)
+    with torch.cuda.device(cache["k"].device):
+        return int(_L.wide_attn_tree_workspace_bytes(ctypes.byref(c), ctypes.byref(d)))
+
+
+def wide_attn_tree(q: torch.Tensor, cache: dict, cache_len: torch.Tensor,
+                   tree_mask: torch.Tensor = None, head_mask: torch.Tensor = None,
+                   draft_len: torch.Tensor = None, scale: float = None, out: torch.Tensor = None,
+                   workspace: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """Attention of draft = T / n_seq new tokens per sequence over the cache
+    that already holds their keys and values (wide_kv_append at cache_len).
+    q bf16 [T][n_q][128] (tokens at any stride); cache_len, draft_len int32
+    [n_seq]; tree_mask int32 words [T][ceil(draft / 32)] (None: a chain);
+    head_mask int32 words [T][ceil(n_kv / 32)] (None: all kept); scale None:
+    1 / sqrt(128).  Returns out bf16 [T][n_q][128]; tokens past draft_len are
+    left as they were (zeros when out is not given)."""
+    if q.dim() != 3 or q.dtype != torch.bfloat16:
+        raise ValueError(f"q must be bfloat16 [T][n_q][head_dim], got {q.dtype} {tuple(q.shape)}")
+    c = _kv_cache(cache)
+    T, n_q, hd = q.shape
+    if c.n_seq == 0 or T % c.n_seq != 0 or T == 0:
+        raise ValueError(f"{T} tokens do not divide into {c.n_seq} sequences")
+    draft = T // c.n_seq
+    if hd != c.head_dim or q.stride(2) != 1 or (q.stride(1) != hd and n_q > 1):
+        raise ValueError(f"the heads of a token of q must be contiguous rows of {c.head_dim}")
+    for name, m, n in (("tree_mask", tree_mask, draft), ("head_mask", head_mask, c.n_kv)):
+        if m is not None and (m.dtype != torch.int32 or tuple(m.shape) != (T, (n + 31) // 32)):
+            raise ValueError(f"{name} must be int32 [{T}][{(n + 31) // 32}], got {m.dtype} "
+                             f"{tuple(m.shape)}")
+    if out is None:
+        make = torch.empty if draft_len is None else torch.zeros
+        out = make((T, n_q, hd), dtype=torch.bfloat16, device=q.device)
+    elif out.dtype != torch.bfloat16 or out.shape != q.shape:
+        raise ValueError(f"out must be bfloat16 {tuple(q.shape)}")
+    dev = _one_device("wide_attn_tree", q=q, cache_len=cache_len, tree_mask=tree_mask,
+                      head_mask=head_mask, draft_len=draft_len, out=out, workspace=workspace,
+                      **_cache_tensors(cache))
+    cl, dl = _index(cache_len, "cache_len", c.n_seq, dev), _index(draft_len, "draft_len", c.n_seq, dev)
+    d = WideAttnTreeDims(draft, q.stride(0) if T > 1 else n_q * hd, n_q,
+                         hd ** -0.5 if scale is None else scale)
+    with torch.cuda.device(dev):
+        need = int(_L.wide_attn_tree_workspace_bytes(ctypes.byref(c), ctypes.byref(d)))
+        if workspace is None or workspace.numel() < need:
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        _check("wide_attn_tree", _L.wide_attn_tree(
+            q.data_ptr(), ctypes.byref(c), cl, dl,
+            None if tree_mask is None else _dev_ptr(tree_mask, "tree_mask"),
+            None if head_mask is None else _dev_ptr(head_mask, "head_mask"),
+            _dev_ptr(out, "out"), ctypes.byref(d), workspace.data_ptr(), workspace.numel(),
+            _stream(stream, dev)))
+    return out

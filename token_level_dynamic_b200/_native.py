@@ -25,6 +25,7 @@ WIDE_DEV_BAD_MASK = 0x1
 WIDE_DEV_TIMEOUT = 0x2
 WIDE_DEV_BAD_ITEM = 0x4
 WIDE_DEV_LAYOUT = 0x8
+WIDE_DEV_BAD_RANGE = 0x10
 WIDE_BF16 = 0
 WIDE_F32 = 1
 WIDE_PATH_AUTO = 0
@@ -32,6 +33,11 @@ WIDE_PATH_DECODE = 1
 WIDE_PATH_PREFILL = 2
 WIDE_ACT_RELU = 0
 WIDE_ACT_SILU = 1
+WIDE_ROPE_HALF = 0
+WIDE_ROPE_INTERLEAVED = 1
+WIDE_KV_BF16 = 0
+WIDE_KV_E4M3 = 1
+WIDE_KV_I8 = 2
 
 
 class WideWorklist(ctypes.Structure):
@@ -62,6 +68,35 @@ class WideLayerWeights(ctypes.Structure):
 class WideRouterDims(ctypes.Structure):
     _fields_ = [("tokens", c_int64), ("hidden", c_int64), ("bottleneck", c_int64),
                 ("groups", c_int64), ("act", c_int32)]
+
+
+class WideRopeConfig(ctypes.Structure):
+    _fields_ = [("rot_dim", c_int32), ("layout", c_int32), ("theta", ctypes.c_double),
+                ("factor", ctypes.c_double), ("low_freq", ctypes.c_double),
+                ("high_freq", ctypes.c_double), ("original_len", c_int64),
+                ("amplitude", ctypes.c_double)]
+
+
+class WideRopeDims(ctypes.Structure):
+    _fields_ = [("tokens", c_int64), ("heads", c_int32), ("head_dim", c_int32), ("dtype", c_int32),
+                ("x_token_stride", c_int64), ("x_head_stride", c_int64),
+                ("out_token_stride", c_int64), ("out_head_stride", c_int64)]
+
+
+class WideKVCache(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
+                ("n_seq", c_int64), ("cap", c_int64), ("n_kv", c_int32), ("head_dim", c_int32),
+                ("kind", c_int32)]
+
+
+class WideKVRows(ctypes.Structure):
+    _fields_ = [("seq_len", c_int64), ("k_token_stride", c_int64), ("k_head_stride", c_int64),
+                ("v_token_stride", c_int64), ("v_head_stride", c_int64)]
+
+
+class WideAttnTreeDims(ctypes.Structure):
+    _fields_ = [("draft", c_int64), ("q_token_stride", c_int64), ("n_q", c_int32),
+                ("scale", ctypes.c_float)]
 
 
 # name -> (restype, argtypes); every symbol include/wide.h declares
@@ -103,6 +138,18 @@ SIGNATURES = {
                                  c_size_t, c_void_p]),
     "wide_route": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                            ctypes.POINTER(WideRouterDims), c_void_p]),
+    "wide_rope": (c_int, [c_void_p, c_void_p, c_void_p, ctypes.POINTER(WideRopeDims),
+                          ctypes.POINTER(WideRopeConfig), c_void_p]),
+    "wide_kv_append": (c_int, [c_void_p, c_void_p, ctypes.POINTER(WideKVCache), c_void_p, c_void_p,
+                               c_void_p, ctypes.POINTER(WideKVRows),
+                               ctypes.POINTER(WideRopeConfig), c_void_p]),
+    "wide_kv_read": (c_int, [c_void_p, c_void_p, ctypes.POINTER(WideKVCache), c_void_p, c_void_p,
+                             ctypes.POINTER(WideKVRows), c_void_p]),
+    "wide_attn_tree_workspace_bytes": (c_size_t, [ctypes.POINTER(WideKVCache),
+                                                  ctypes.POINTER(WideAttnTreeDims)]),
+    "wide_attn_tree": (c_int, [c_void_p, ctypes.POINTER(WideKVCache), c_void_p, c_void_p, c_void_p,
+                               c_void_p, c_void_p, ctypes.POINTER(WideAttnTreeDims), c_void_p,
+                               c_size_t, c_void_p]),
 }
 
 _lib = None

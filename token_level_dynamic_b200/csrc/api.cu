@@ -393,6 +393,8 @@ const char *wide_status_string(int code)
         return "device: work item out of range";
     case WIDE_DEV_LAYOUT:
         return "device: shared-memory alignment precondition failed";
+    case WIDE_DEV_BAD_RANGE:
+        return "device: length, count or cache position out of range";
     default:
         return code > 0 ? "device: several error bits" : "unknown status";
     }

@@ -1,0 +1,209 @@
+// attn_tree.cuh -- what the kernels of wide_attn_tree share: the division of
+// the work over the GPU, made on the device from the lengths and masks, and
+// the records that join the parts of a run.
+//
+// A unit is a (sequence, KV head).  Its rows are the query heads of the
+// tokens that keep the head group, rep per token, in token order; a run is
+// `rt` of those rows over the unit's keys, in blocks of `bk` keys.  All runs'
+// blocks, unit after unit, form one line of `total` blocks, and CTA c of n
+// takes blocks [c total / n, (c + 1) total / n): equal work for any mixture
+// of lengths and masks, without a value read back by the host.  A CTA that
+// holds only a part of a run (at most its first and its last segment) leaves
+// the part's unnormalised output, maximum and sum in its two workspace slots;
+// the CTA that holds a run's first block records the run's extent, and
+// attn_tree_join adds the parts in order, so results never depend on timing.
+#pragma once
+
+#include "common.cuh"
+
+namespace wide {
+
+constexpr int kTreeHD = 128;
+constexpr int kTreeMaxUnits = 4096;
+constexpr int kTreeMaxDraft = 1024;
+
+struct TreeArgs {
+    const __nv_bfloat16 *q;            // [T][n_q][128], q_stride apart
+    const void *k, *v;                 // caches
+    const uint8_t *ks, *vs;
+    const int32_t *cache_len, *draft_len;
+    const uint32_t *tree, *heads;
+    __nv_bfloat16 *out;
+    int n_seq, draft, n_q, n_kv, rep, Wt, Wh;
+    int64_t cap, q_stride;
+    float scale_log2;
+    // parts: slot 2 c (CTA c's first segment) and 2 c + 1
+    float *part_o;                     // [2 n][rt][128]
+    float2 *part_ml;                   // [2 n][rt] (max in log2 units, sum)
+    int4 *joins;                       // [n]: run starting in CTA c: (last CTA, first slot, rows, 0); rows 0: none
+    int32_t *join_rows;                // [n][rt] output row of each row of that run
+    int32_t *status;
+};
+
+// Sequence s: its earlier and new positions; both 0 if its lengths are bad.
+__device__ __forceinline__ int2 tree_lens(const TreeArgs &a, int s, bool report)
+{
+    const int cl = a.cache_len[s], dl = a.draft_len ? a.draft_len[s] : a.draft;
+    if (cl < 0 || dl < 0 || dl > a.draft || (int64_t)cl + dl > a.cap) {
+        if (report)
+            set_status(a.status, WIDE_DEV_BAD_RANGE);
+        return make_int2(0, 0);
+    }
+    return make_int2(cl, dl);
+}
+
+// cum[u] = blocks before unit u (u = s * n_kv + j; cum[U] = all), cnt[u] =
+// tokens that keep the group.  All threads of the CTA; ends with a barrier.
+template <int THREADS>
+__device__ void tree_plan(const TreeArgs &a, int rt, int bk, uint32_t *cum, uint16_t *cnt)
+{
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int U = a.n_seq * a.n_kv;
+    for (int s = warp; s < a.n_seq; s += THREADS / 32) {
+        const int2 len = tree_lens(a, s, blockIdx.x == 0 && lane == 0);
+        const uint32_t nb = (uint32_t)((len.x + len.y + bk - 1) / bk);
+        for (int w = 0; w < (a.n_kv + 31) / 32; ++w) {
+            const int nj = min(32, a.n_kv - 32 * w);
+            int mine = 0;              // lane j: tokens that keep group 32 w + j
+            if (!a.heads) {
+                mine = len.y;
+            } else {
+                for (int t0 = 0; t0 < len.y; t0 += 32) {
+                    const int t = t0 + lane;
+                    const uint32_t bits =
+                        t < len.y ? a.heads[((size_t)s * a.draft + t) * a.Wh + w] : 0u;
+                    for (int j = 0; j < nj; ++j) {
+                        const int c = __popc(__ballot_sync(0xffffffffu, (bits >> j) & 1u));
+                        mine += lane == j ? c : 0;
+                    }
+                }
+            }
+            if (lane < nj) {
+                const int u = s * a.n_kv + 32 * w + lane;
+                cnt[u] = (uint16_t)mine;
+                cum[u + 1] = (uint32_t)((mine * a.rep + rt - 1) / rt) * nb;
+            }
+        }
+    }
+    if (tid == 0)
+        cum[0] = 0;
+    __syncthreads();
+    // inclusive scan of cum[1..U]: each thread a stretch, then the stretches
+    __shared__ uint32_t part[THREADS / 32];
+    const int per = (U + THREADS - 1) / THREADS;
+    const int lo = min(U, tid * per), hi = min(U, lo + per);
+    uint32_t sum = 0;
+    for (int i = lo; i < hi; ++i)
+        sum += cum[i + 1];
+    uint32_t inc = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off)
+            inc += o;
+    }
+    if (lane == 31)
+        part[warp] = inc;
+    __syncthreads();
+    uint32_t before = inc - sum;
+    for (int w = 0; w < warp; ++w)
+        before += part[w];
+    for (int i = lo; i < hi; ++i) {
+        before += cum[i + 1];
+        cum[i + 1] = before;
+    }
+    __syncthreads();
+}
+
+// The unit that holds block b: the largest u with cum[u] <= b.
+__device__ __forceinline__ int tree_unit(const uint32_t *cum, int U, uint32_t b)
+{
+    int lo = 0, hi = U;                // cum[lo] <= b < cum[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cum[mid] <= b)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// Owner of block b when n CTAs share `total` blocks.
+__device__ __forceinline__ int tree_owner(uint32_t b, uint32_t total, int n)
+{
+    return (int)((((uint64_t)b + 1) * (uint64_t)n - 1) / total);
+}
+
+// Tokens of the unit that keep the group, numbers [from, to) of them, into
+// tok[]; by one whole warp.
+__device__ __forceinline__ void tree_tokens(const TreeArgs &a, int s, int j, int dl, int from,
+                                            int to, int32_t *tok)
+{
+    const int lane = threadIdx.x & 31;
+    int seen = 0;
+    for (int t0 = 0; t0 < dl && seen < to; t0 += 32) {
+        const int t = t0 + lane;
+        const bool on =
+            t < dl &&
+            (!a.heads ||
+             ((a.heads[((size_t)s * a.draft + t) * a.Wh + (j >> 5)] >> (j & 31)) & 1u));
+        const uint32_t b = __ballot_sync(0xffffffffu, on);
+        const int at = seen + __popc(b & ((1u << lane) - 1u));
+        if (on && at >= from && at < to)
+            tok[at - from] = t;
+        seen += __popc(b);
+    }
+}
+
+// Whether new token t of sequence s attends new token j.
+__device__ __forceinline__ bool tree_sees(const TreeArgs &a, int s, int t, int j)
+{
+    if (!a.tree)
+        return j <= t;
+    return (a.tree[((size_t)s * a.draft + t) * a.Wt + (j >> 5)] >> (j & 31)) & 1u;
+}
+
+// Zeros for the pairs of new token and head group that are skipped; the CTAs
+// share the pairs.
+template <int THREADS> __device__ void tree_zero_skipped(const TreeArgs &a)
+{
+    if (!a.heads)
+        return;
+    const int lane = threadIdx.x & 31;
+    const int64_t pairs = (int64_t)a.n_seq * a.draft * a.n_kv;
+    const int64_t warps = (int64_t)gridDim.x * (THREADS / 32);
+    for (int64_t p0 = ((int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5)) * 32; p0 < pairs;
+         p0 += warps * 32) {
+        const int64_t p = p0 + lane;
+        bool zero = false;
+        if (p < pairs) {
+            const int64_t t = p / a.n_kv;
+            const int j = (int)(p - t * a.n_kv), s = (int)(t / a.draft);
+            zero = (int)(t - (int64_t)s * a.draft) < tree_lens(a, s, false).y &&
+                   !((a.heads[(size_t)t * a.Wh + (j >> 5)] >> (j & 31)) & 1u);
+        }
+        uint32_t todo = __ballot_sync(0xffffffffu, zero);
+        while (todo) {
+            const int64_t z = p0 + __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int64_t t = z / a.n_kv;
+            const int j = (int)(z - t * a.n_kv);
+            uint4 *o = reinterpret_cast<uint4 *>(a.out + (t * a.n_q + (int64_t)j * a.rep) * kTreeHD);
+            for (int i = lane; i < a.rep * (kTreeHD / 8); i += 32)
+                o[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+}
+
+// Waits for the kernels this launch depends on (programmatic launch).
+__device__ __forceinline__ void grid_dependency_wait()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void grid_launch_dependents()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+}  // namespace wide

@@ -117,6 +117,11 @@ enum KernelId : int32_t {
     KID_DECODE_FFN_SPLIT = 18,
     KID_DECODE_FFN_TC = 19,
     KID_FFN_PACK = 20,
+    KID_ROPE = 21,
+    KID_KV_APPEND = 22,
+    KID_KV_READ = 23,
+    KID_ATTN_TREE = 24,
+    KID_ATTN_TREE_JOIN = 25,
 };
 
 // Pointers of one masked-layer call (FFN pointers unused when !ffn).
@@ -245,6 +250,20 @@ int rmsnorm_f32_launch(const float *x, const void *gamma, void *y, int T, int H,
 bool layer_decode_supported(const wide_layer_dims *d);
 size_t layer_decode_workspace(const wide_layer_dims *d);
 int layer_decode_launch(const LayerPtrs &p, const wide_layer_dims *d, void *ws, cudaStream_t s);
+
+// Whether rows of `len` elements, nt x nh of them at the given strides
+// (elements), lie apart from one another.
+inline bool rows_apart(int64_t nt, int64_t ts, int64_t nh, int64_t hs, int64_t len)
+{
+    if (nt > 1 && ts < len)
+        return false;
+    if (nh > 1 && hs < len)
+        return false;
+    return nt <= 1 || nh <= 1 || ts >= (nh - 1) * hs + len || hs >= (nt - 1) * ts + len;
+}
+
+// Argument checks of a cache (kv_cache.cu).
+int kv_cache_check(const wide_kv_cache *c);
 
 size_t ffn_decode_workspace(const wide_ffn_dims *d);
 // bf16 decode GEMVs for T <= 32 tokens (one chunk): gate/up writes fp32 h for

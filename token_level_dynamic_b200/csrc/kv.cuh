@@ -1,0 +1,90 @@
+// kv.cuh -- the 8-bit cache format: device helpers shared by the cache
+// writer and reader (kv_cache.cu) and the attention over it.
+//
+// A block of 32 elements has one scale byte b, the scale is 2^(b - 127).
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace wide {
+
+constexpr int kKvHD = 128;          // elements of a row
+constexpr int kKvBlock = 32;        // elements per scale
+constexpr int kKvMinExp = -124;     // smallest scale: keeps 2^-9 of it (e4m3's step) a bf16 number
+
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Scale byte of a block whose largest magnitude is `top` (bits of a
+// non-negative fp32): the smallest exponent e >= kKvMinExp with
+// top <= kMax * 2^e; 0 for a block of zeros, 255 for one that is not finite.
+// top = 1.f * 2^p with kMax = 1.m * 2^q gives e = p - q, one more when the
+// mantissa is above kMax's (448 = 1.75 * 2^8, 127 = 1.984375 * 2^6).
+template <int KIND>
+__device__ __forceinline__ uint32_t kv_scale_byte(uint32_t top)
+{
+    constexpr int kQ = KIND == WIDE_KV_E4M3 ? 8 : 6;
+    constexpr uint32_t kMant = KIND == WIDE_KV_E4M3 ? 0x600000u : 0x7E0000u;
+    if (top >= 0x7f800000u)
+        return 255u;
+    if (top == 0u)
+        return 0u;
+    const int e = (int)(top >> 23) - 127 - kQ + ((top & 0x7fffffu) > kMant ? 1 : 0);
+    return (uint32_t)(max(e, kKvMinExp) + 127);
+}
+
+// 8 elements in the code of a block with scale byte b (0 and 255: zeros).
+// x * 2^-e is exact (or far below half the smallest code), so each code is
+// the correctly rounded one.
+template <int KIND>
+__device__ __forceinline__ uint2 kv_encode8(const float (&x)[8], uint32_t b)
+{
+    const float r = (b == 0u || b == 255u) ? 0.f : exp2i(127 - (int)b);
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if constexpr (KIND == WIDE_KV_E4M3) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+                make_float2(x[4 * i] * r, x[4 * i + 1] * r), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+                make_float2(x[4 * i + 2] * r, x[4 * i + 3] * r), __NV_SATFINITE, __NV_E4M3);
+            w[i] = lo | (hi << 16);
+        } else {
+            w[i] = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[i] |= ((uint32_t)__float2int_rn(x[4 * i + k] * r) & 255u) << (8 * k);
+        }
+    }
+    return b == 255u ? make_uint2(0u, 0u) : make_uint2(w[0], w[1]);
+}
+
+// Multiplier of a block with scale byte b (byte 0 stands for zeros).
+__device__ __forceinline__ float kv_scale(uint32_t b)
+{
+    return b == 255u ? __uint_as_float(0x7fffffffu) : exp2i(max((int)b, 1) - 127);
+}
+
+// 4 codes (one word) as fp32 numbers times `scale`.
+template <int KIND>
+__device__ __forceinline__ void kv_decode4(uint32_t w, float scale, float (&f)[4])
+{
+    if constexpr (KIND == WIDE_KV_E4M3) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                (__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3);
+            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            f[2 * i] = v.x * scale;
+            f[2 * i + 1] = v.y * scale;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = (float)(int)(int8_t)(w >> (8 * i)) * scale;
+    }
+}
+
+}  // namespace wide

@@ -131,6 +131,16 @@ const char *wide_kernel_name(int32_t id)
         return "decode_ffn_tcgen05";
     case KID_FFN_PACK:
         return "ffn_pack";
+    case KID_ROPE:
+        return "rope_rows";
+    case KID_KV_APPEND:
+        return "kv_append_rows";
+    case KID_KV_READ:
+        return "kv_read_rows";
+    case KID_ATTN_TREE:
+        return "attn_tree";
+    case KID_ATTN_TREE_JOIN:
+        return "attn_tree_join";
     default:
         return "?";
     }

@@ -1,0 +1,232 @@
+// rope.cu -- wide_rope: the rotation of the first rot_dim elements of every
+// head by its token's position (formula in wide.h).
+//
+// Each element is read and written once, so the kernel is bound by memory
+// (at small token counts by its launch).  A CTA takes a few tokens: its
+// threads first compute the tokens' (cos, sin) pairs into shared memory, each
+// once for all heads (the double product and the reduction to one turn cost
+// more than rotating a pair, and a token of 40 heads uses every angle 40
+// times), then rotate 16 bytes of the a elements and 16 of the b elements per
+// step (half layout) or 16 bytes of whole pairs (interleaved).  Rows that are
+// not made of aligned 16-byte pieces go the same way one pair at a time.
+#include "host.h"
+#include "rope.cuh"
+
+#include <math.h>
+
+namespace wide {
+
+bool rope_table(const wide_rope_config *c, RopeTable *t)
+{
+    if (!c || c->rot_dim < 2 || c->rot_dim > 2 * kRopeMaxPairs || (c->rot_dim & 1) ||
+        (c->layout != WIDE_ROPE_HALF && c->layout != WIDE_ROPE_INTERLEAVED) ||
+        !(c->theta > 0.0) || !isfinite(c->theta) || !(c->factor > 0.0) || !isfinite(c->factor) ||
+        !(c->amplitude > 0.0) || !isfinite(c->amplitude) || c->original_len < 0)
+        return false;
+    const bool ramp = c->factor != 1.0 && c->original_len > 0;
+    if (ramp && (!(c->low_freq >= 0.0) || !(c->high_freq > c->low_freq) || !isfinite(c->high_freq)))
+        return false;
+    const double two_pi = 6.283185307179586476925286766559;
+    for (int i = 0; i < kRopeMaxPairs; ++i) {
+        double f = 0.0;
+        if (i < c->rot_dim / 2) {
+            f = pow(c->theta, -2.0 * i / c->rot_dim);
+            if (ramp) {
+                const double r = (double)c->original_len * f / two_pi;
+                double g = (r - c->low_freq) / (c->high_freq - c->low_freq);
+                g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
+                f *= g + (1.0 - g) / c->factor;
+            } else {
+                f /= c->factor;
+            }
+        }
+        t->turns[i] = f / two_pi;
+    }
+    t->amplitude = (float)c->amplitude;
+    return true;
+}
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct RopeArgs {
+    const void *x;
+    const int32_t *pos;
+    void *out;
+    int64_t xt, xh, ot, oh;        // token and head strides, elements
+    int64_t tokens;
+    int heads, head_dim, pairs;    // pairs = rot_dim / 2
+    int tok_per_cta, heads_per_cta;
+    int rest;                      // elements past the rotated part to copy (0 in place)
+};
+
+template <typename T, int VEC> struct Piece;    // VEC elements, moved as one access
+template <> struct Piece<__nv_bfloat16, 8> {
+    uint4 w;
+    __device__ void get(float (&f)[8]) const { bf16x8_to_f32(w, f); }
+    __device__ void set(const float (&f)[8])
+    {
+        uint32_t *o = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            o[i] = *reinterpret_cast<const uint32_t *>(&p);
+        }
+    }
+};
+template <> struct Piece<float, 4> {
+    float4 w;
+    __device__ void get(float (&f)[4]) const { f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w; }
+    __device__ void set(const float (&f)[4]) { w = make_float4(f[0], f[1], f[2], f[3]); }
+};
+template <typename T> struct Piece<T, 1> {
+    T w;
+    __device__ void get(float (&f)[1]) const { f[0] = to_f32(w); }
+    __device__ void set(const float (&f)[1]) { w = from_f32<T>(f[0]); }
+};
+template <typename T> struct Piece<T, 2> {      // one interleaved pair, any alignment
+    T a, b;
+    __device__ void get(float (&f)[2]) const { f[0] = to_f32(a), f[1] = to_f32(b); }
+    __device__ void set(const float (&f)[2]) { a = from_f32<T>(f[0]), b = from_f32<T>(f[1]); }
+};
+
+// VEC: elements per access of one stream; half layout: 16 bytes or 1,
+// interleaved: 16 bytes or one pair.
+template <typename T, int VEC, bool INTER>
+__global__ void __launch_bounds__(kThreads)
+    rope_rows(const __grid_constant__ RopeTable tab, const RopeArgs a)
+{
+    extern __shared__ float2 cs[];          // [tok_per_cta][pairs]
+    const int64_t t0 = (int64_t)blockIdx.x * a.tok_per_cta;
+    const int nt = (int)min((int64_t)a.tok_per_cta, a.tokens - t0);
+    const int h0 = (int)blockIdx.y * a.heads_per_cta;
+    const int nh = min(a.heads_per_cta, a.heads - h0);
+    for (int i = threadIdx.x; i < nt * a.pairs; i += kThreads) {
+        const int t = i / a.pairs, p = i - t * a.pairs;
+        cs[i] = rope_cos_sin(tab.turns[p], a.pos[t0 + t], tab.amplitude);
+    }
+    __syncthreads();
+    using P = Piece<T, VEC>;
+    constexpr int kPer = INTER ? VEC / 2 : VEC;     // pairs per step
+    const int steps = a.pairs / kPer;               // of one row
+    const int rest = a.rest / VEC;
+    const int per_row = steps + rest;
+    const int items = nt * nh * per_row;
+    const T *x = static_cast<const T *>(a.x);
+    T *out = static_cast<T *>(a.out);
+#pragma unroll 2
+    for (int i = threadIdx.x; i < items; i += kThreads) {
+        const int row = i / per_row, c = i - row * per_row;
+        const int t = row / nh, h = row - t * nh;
+        const T *xr = x + (t0 + t) * a.xt + (int64_t)(h0 + h) * a.xh;
+        T *orow = out + (t0 + t) * a.ot + (int64_t)(h0 + h) * a.oh;
+        if (c >= steps) {
+            const int e = 2 * a.pairs + (c - steps) * VEC;
+            *reinterpret_cast<P *>(orow + e) = *reinterpret_cast<const P *>(xr + e);
+            continue;
+        }
+        const float2 *w = cs + t * a.pairs + c * kPer;
+        if constexpr (INTER) {
+            P p = *reinterpret_cast<const P *>(xr + c * VEC);
+            float v[VEC];
+            p.get(v);
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+                rope_pair(v[2 * k], v[2 * k + 1], w[k]);
+            p.set(v);
+            *reinterpret_cast<P *>(orow + c * VEC) = p;
+        } else {
+            P pa = *reinterpret_cast<const P *>(xr + c * VEC);
+            P pb = *reinterpret_cast<const P *>(xr + a.pairs + c * VEC);
+            float va[VEC], vb[VEC];
+            pa.get(va);
+            pb.get(vb);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k)
+                rope_pair(va[k], vb[k], w[k]);
+            pa.set(va);
+            pb.set(vb);
+            *reinterpret_cast<P *>(orow + c * VEC) = pa;
+            *reinterpret_cast<P *>(orow + a.pairs + c * VEC) = pb;
+        }
+    }
+}
+
+template <typename T>
+int rope_launch(RopeArgs a, const RopeTable &tab, bool inter, cudaStream_t s)
+{
+    constexpr int V = 16 / (int)sizeof(T);
+    const bool vec = (a.pairs * (inter ? 2 : 1)) % V == 0 && a.head_dim % V == 0 && a.xt % V == 0 &&
+                     a.xh % V == 0 && a.ot % V == 0 && a.oh % V == 0 && aligned16(a.x) &&
+                     aligned16(a.out) && (2 * a.pairs) % V == 0;
+    // tokens: enough angles to occupy the CTA; heads: split until the grid
+    // covers the GPU (few tokens), down to about one step per thread
+    a.tok_per_cta = a.pairs >= kThreads ? 1 : kThreads / a.pairs;
+    while (a.tok_per_cta > 1 && (a.tokens + a.tok_per_cta - 1) / a.tok_per_cta < 296)
+        a.tok_per_cta = (a.tok_per_cta + 1) / 2;
+    const int64_t bx = (a.tokens + a.tok_per_cta - 1) / a.tok_per_cta;
+    const int steps = vec ? (a.pairs * (inter ? 2 : 1)) / V : a.pairs;
+    a.heads_per_cta = a.heads;
+    while (a.heads_per_cta > 1 && bx * ((a.heads + a.heads_per_cta - 1) / a.heads_per_cta) < 296 &&
+           a.tok_per_cta * a.heads_per_cta * steps > kThreads)
+        a.heads_per_cta = (a.heads_per_cta + 1) / 2;
+    const dim3 grid((unsigned)bx, (unsigned)((a.heads + a.heads_per_cta - 1) / a.heads_per_cta));
+    const size_t smem = (size_t)a.tok_per_cta * a.pairs * sizeof(float2);
+    LaunchScope scope(KID_ROPE, s);
+    if (inter && vec)
+        rope_rows<T, V, true><<<grid, kThreads, smem, s>>>(tab, a);
+    else if (inter)
+        rope_rows<T, 2, true><<<grid, kThreads, smem, s>>>(tab, a);
+    else if (vec)
+        rope_rows<T, V, false><<<grid, kThreads, smem, s>>>(tab, a);
+    else
+        rope_rows<T, 1, false><<<grid, kThreads, smem, s>>>(tab, a);
+    return launch_status();
+}
+
+}  // namespace
+}  // namespace wide
+
+using namespace wide;
+
+extern "C" int wide_rope(const void *d_x, const int32_t *d_positions, void *d_out,
+                         const wide_rope_dims *d, const wide_rope_config *rope, void *stream)
+{
+    RopeTable tab;
+    if (!d || d->tokens < 0 || d->heads <= 0 || d->head_dim <= 0 ||
+        (d->dtype != WIDE_BF16 && d->dtype != WIDE_F32) || !rope_table(rope, &tab) ||
+        rope->rot_dim > d->head_dim || d->x_token_stride < 0 || d->x_head_stride < 0 ||
+        (d->tokens > 0 && !rows_apart(d->tokens, d->out_token_stride, d->heads,
+                                      d->out_head_stride, d->head_dim)))
+        return WIDE_EINVAL;
+    if (d->tokens == 0)
+        return WIDE_OK;
+    if (!d_x || !d_positions || !d_out)
+        return WIDE_EINVAL;
+    const uintptr_t es = d->dtype == WIDE_BF16 ? 2 : 4;
+    if (d->head_dim > 1024 || d->head_dim % 2 || d->tokens > (1 << 28) || d->heads > 65535 || (int64_t)d->heads * d->head_dim > (1 << 20) ||
+        reinterpret_cast<uintptr_t>(d_x) % es || reinterpret_cast<uintptr_t>(d_out) % es ||
+        (reinterpret_cast<uintptr_t>(d_positions) & 3u))
+        return WIDE_EUNSUPPORTED;
+    RopeArgs a = {};
+    a.x = d_x;
+    a.pos = d_positions;
+    a.out = d_out;
+    // a stride of a dimension of one element is never used: make it neutral
+    a.xt = d->tokens > 1 ? d->x_token_stride : 0;
+    a.xh = d->heads > 1 ? d->x_head_stride : 0;
+    a.ot = d->tokens > 1 ? d->out_token_stride : 0;
+    a.oh = d->heads > 1 ? d->out_head_stride : 0;
+    a.tokens = d->tokens;
+    a.heads = d->heads;
+    a.head_dim = d->head_dim;
+    a.pairs = rope->rot_dim / 2;
+    a.rest = d_out == d_x ? 0 : d->head_dim - rope->rot_dim;
+    if (d_out == d_x && (a.xt != a.ot || a.xh != a.oh))
+        return WIDE_EINVAL;
+    const bool inter = rope->layout == WIDE_ROPE_INTERLEAVED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return d->dtype == WIDE_BF16 ? rope_launch<__nv_bfloat16>(a, tab, inter, s)
+                                 : rope_launch<float>(a, tab, inter, s);
+}
