@@ -23,26 +23,10 @@
 namespace wide {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kRows = 16;              // rows of a run
+constexpr int kRunCost = 2;            // blocks' time that a run costs beside its blocks
 constexpr int kOPitch = kTreeHD + 4;   // floats; row pitch of the warps' outputs when merged
-
-__device__ __forceinline__ float exp2_sfu(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint4 load_stream(const void *p)
-{
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1)
@@ -51,53 +35,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
-{
-    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&p);
-}
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
-{
-    uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
-{
-    uint32_t d;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
-// Multiplier that turns a code, moved into bf16 bits, into its value.  e4m3:
-// the bits stand for value * 2^-120, so the multiplier is 2^(b - 127 + 120);
-// above 2^127 (b > 134) the rest goes into a second one, kv_mult_high.
-template <int KIND> __device__ __forceinline__ uint32_t kv_mult(uint32_t b)
-{
-    if (b == 255u)
-        return 0x7fffu;
-    return (KIND == WIDE_KV_E4M3 ? min(b + 120u, 254u) : b) << 7;
-}
-__device__ __forceinline__ uint32_t kv_mult_high(uint32_t b)
-{
-    return (b > 134u && b < 255u ? b - 7u : 127u) << 7;
-}
-
-// Two codes, in the bytes of t that the kind wants (e4m3: the high byte of
-// each half; i8: the low byte; the other byte is ignored), as bf16 times mult.
-template <int KIND> __device__ __forceinline__ uint32_t kv_pair(uint32_t t, uint32_t mult)
-{
-    if constexpr (KIND == WIDE_KV_E4M3) {
-        // sign, exponent and mantissa to bf16's places: s eeee mmm -> s 0000eeee mmm0000
-        return mul_bf16x2(((t >> 4) & 0x07f007f0u) | (t & 0x80008000u), mult);
-    } else {
-        // 128 + (x & 127) as bf16, minus 128, or minus 256 if the sign bit is set
-        const uint32_t u = (t & 0x007f007fu) | 0x43004300u, z = (t & 0x00800080u) | 0x43004300u;
-        return mul_bf16x2(sub_bf16x2(u, z), mult);
-    }
 }
 
 template <int KIND> struct TreeCfg {
@@ -170,9 +107,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
     __shared__ int32_t slist[kRows];
     __shared__ uint32_t sbad[kTreeMaxDraft / 32];                      // new positions with a value that is not finite
     __shared__ int s_any_bad;
+    __shared__ uint32_t spart[kWarps];
 
     tree_zero_skipped<kThreads>(a);
-    tree_plan<kThreads>(a, kRows, C::kBK, cum, cnt);
+    tree_plan<kThreads>(a, kRows, C::kBK, kRunCost, cum, cnt, spart);
     const uint32_t total = cum[U];
     const int n_cta = (int)min((uint32_t)gridDim.x, total);
     const int me = (int)blockIdx.x;
@@ -191,10 +129,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
         const int s = u / a.n_kv, j = u - s * a.n_kv;
         const int2 len = tree_lens(a, s, false);
         const int nkeys = len.x + len.y;
-        const int nb = (nkeys + C::kBK - 1) / C::kBK;
-        const int run = (int)(b - cum[u]) / nb;
-        const int blk0 = (int)(b - cum[u]) - run * nb;
-        const int blk1 = (int)min((uint32_t)nb, (uint32_t)blk0 + (end - b));
+        const int nb = (nkeys + C::kBK - 1) / C::kBK, per = nb + kRunCost;
+        const int run = (int)(b - cum[u]) / per;
+        const int pos = (int)(b - cum[u]) - run * per;
+        const int stop = (int)min((uint32_t)per, (uint32_t)pos + (end - b));
+        b += (uint32_t)(stop - pos);
+        const int blk0 = max(pos - kRunCost, 0), blk1 = max(stop - kRunCost, 0);
+        if (blk0 == blk1)
+            continue;
         const int nrows = min(kRows, (int)cnt[u] * a.rep - run * kRows);
 
         // rows of the run: their tokens
@@ -461,12 +403,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
             }
         __syncthreads();
         const bool whole = blk0 == 0 && blk1 == nb;
-        const int slot = 2 * me + (b != first);
+        const int slot = 2 * me + (blk0 == 0);
         if (!whole && blk0 == 0) {              // the run starts here: record its extent
             joined = true;
             if (tid == 0)
                 a.joins[me] = make_int4(
-                    tree_owner(cum[u] + (uint32_t)(run + 1) * nb - 1, total, n_cta), slot, nrows, 0);
+                    tree_owner(cum[u] + (uint32_t)(run + 1) * per - 1, total, n_cta), slot, nrows, 0);
             if (tid < nrows)
                 a.join_rows[me * kRows + tid] = (int32_t)(((int64_t)s * a.draft + stok[tid]) * a.n_q +
                                                           j * a.rep + (run * kRows + tid) % a.rep);
@@ -532,7 +474,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
                     a.part_ml[(int64_t)slot * kRows + r] = make_float2(M, L);
             }
         }
-        b += (uint32_t)(blk1 - blk0);
     }
     if (!joined && tid == 0)
         a.joins[me] = make_int4(0, 0, 0, 0);
@@ -553,7 +494,7 @@ __global__ void __launch_bounds__(256)
     if (r >= jn.z)
         return;
     const int parts = jn.x - c0 + 1;
-    // part i > 0 is the first segment of CTA c0 + i
+    // part 0 is in its CTA's second slot, the others in their CTAs' first
     float M = -INFINITY;
     for (int i = lane; i < parts; i += 32)
         M = fmaxf(M, part_ml[(int64_t)(i ? 2 * (c0 + i) : jn.y) * ROWS + r].x);
@@ -619,7 +560,23 @@ int sm_count()
     return n;
 }
 
-constexpr int kCtasPerSm = 2;
+constexpr int kCtasPerSm = 2;          // of attn_tree_rows
+
+// Which kernel takes the call, by the rows that a unit can have: rows of a run
+// and CTAs.  Up to 16 rows attn_tree_rows, which needs no shared memory for the
+// keys (one token over 2048 keys 20 us and 29 ragged sequences in int8 104 us,
+// against 20 and 106 of attn_tree_tiles); above, its 16 rows a pass read and
+// convert the cache again (16 tokens over 131072 keys in e4m3: 354 us against 115).
+struct TreeChoice {
+    int rt, n;
+};
+TreeChoice tree_choice(const wide_kv_cache *c, const wide_attn_tree_dims *d)
+{
+    const int64_t rows = d->draft * (d->n_q / c->n_kv);
+    if (rows <= kRows)
+        return {kRows, kCtasPerSm * sm_count()};
+    return {rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256, sm_count()};
+}
 
 int tree_check(const wide_kv_cache *c, const wide_attn_tree_dims *d)
 {
@@ -634,8 +591,8 @@ int tree_check(const wide_kv_cache *c, const wide_attn_tree_dims *d)
     if (d->draft > kTreeMaxDraft || d->n_q / c->n_kv > 32 ||
         c->n_seq * c->n_kv > kTreeMaxUnits || d->q_token_stride % 8 != 0 ||
         c->n_seq * d->draft * d->n_q > (1 << 30) ||
-        // the work's blocks are counted in 32 bits
-        c->n_seq * c->n_kv * ((rows + kRows - 1) / kRows) * (c->cap / 32 + 1) > (int64_t)0x7fffffff)
+        // the work's places are counted in 32 bits
+        c->n_seq * c->n_kv * ((rows + kRows - 1) / kRows) * (c->cap / 32 + 3) > (int64_t)0x7fffffff)
         return WIDE_EUNSUPPORTED;
     return WIDE_OK;
 }
@@ -683,7 +640,8 @@ size_t wide_attn_tree_workspace_bytes(const wide_kv_cache *cache, const wide_att
 {
     if (tree_check(cache, d) != WIDE_OK)
         return 0;
-    return tree_ws(kCtasPerSm * sm_count(), kRows, nullptr).total;
+    const TreeChoice ch = tree_choice(cache, d);
+    return tree_ws(ch.n, ch.rt, nullptr).total;
 }
 
 int wide_attn_tree(const void *d_q, const wide_kv_cache *cache, const int32_t *d_cache_len,
@@ -705,8 +663,8 @@ int wide_attn_tree(const void *d_q, const wide_kv_cache *cache, const int32_t *d
             return WIDE_EUNSUPPORTED;
     if (!aligned16(d_q) || !aligned16(d_out) || (reinterpret_cast<uintptr_t>(d_workspace) & 255u))
         return WIDE_EUNSUPPORTED;
-    const int n = kCtasPerSm * sm_count();
-    const TreeWs w = tree_ws(n, kRows, d_workspace);
+    const TreeChoice ch = tree_choice(cache, d);
+    const TreeWs w = tree_ws(ch.n, ch.rt, d_workspace);
     if (workspace_bytes < w.total)
         return WIDE_EWORKSPACE;
     TreeArgs a = {};
@@ -736,12 +694,20 @@ int wide_attn_tree(const void *d_q, const wide_kv_cache *cache, const int32_t *d
     a.join_rows = w.join_rows;
     a.status = status_ptr();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int rc = cache->kind == WIDE_KV_BF16   ? tree_rows_launch<WIDE_KV_BF16>(a, n, s)
-                   : cache->kind == WIDE_KV_E4M3 ? tree_rows_launch<WIDE_KV_E4M3>(a, n, s)
-                                                 : tree_rows_launch<WIDE_KV_I8>(a, n, s);
+    if (ch.rt != kRows) {
+        if (int rc = attn_tree_tiles_launch(a, cache->kind, ch.rt, ch.n, s))
+            return rc;
+        return ch.rt == 32    ? tree_join_launch<32>(a, ch.n, s)
+               : ch.rt == 64  ? tree_join_launch<64>(a, ch.n, s)
+               : ch.rt == 128 ? tree_join_launch<128>(a, ch.n, s)
+                              : tree_join_launch<256>(a, ch.n, s);
+    }
+    const int rc = cache->kind == WIDE_KV_BF16   ? tree_rows_launch<WIDE_KV_BF16>(a, ch.n, s)
+                   : cache->kind == WIDE_KV_E4M3 ? tree_rows_launch<WIDE_KV_E4M3>(a, ch.n, s)
+                                                 : tree_rows_launch<WIDE_KV_I8>(a, ch.n, s);
     if (rc)
         return rc;
-    return tree_join_launch<kRows>(a, n, s);
+    return tree_join_launch<kRows>(a, ch.n, s);
 }
 
 }  // extern "C"

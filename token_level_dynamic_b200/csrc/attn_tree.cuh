@@ -4,20 +4,23 @@
 //
 // A unit is a (sequence, KV head).  Its rows are the query heads of the
 // tokens that keep the head group, rep per token, in token order; a run is
-// `rt` of those rows over the unit's keys, in blocks of `bk` keys.  All runs'
-// blocks, unit after unit, form one line of `total` blocks, and CTA c of n
-// takes blocks [c total / n, (c + 1) total / n): equal work for any mixture
-// of lengths and masks, without a value read back by the host.  A CTA that
-// holds only a part of a run (at most its first and its last segment) leaves
-// the part's unnormalised output, maximum and sum in its two workspace slots;
-// the CTA that holds a run's first block records the run's extent, and
-// attn_tree_join adds the parts in order, so results never depend on timing.
+// `rt` of those rows over the unit's keys, in blocks of `bk` keys.  A run takes
+// `rc` places for what it costs beside its blocks, then one for each block (two
+// in a run of more than 128 rows).  All runs' places, unit after unit, form one line of `total`, and
+// CTA c of n takes the blocks whose (first) place is in [c total / n, (c + 1) total / n): equal
+// work for any mixture of lengths and masks, without a value read back by the
+// host.  A CTA that holds only a part of a run (at most its first and its last
+// segment) leaves the part's unnormalised output, maximum and sum in one of its
+// two workspace slots, the first if the run began in an earlier CTA; the CTA
+// that holds a run's first block records the run's extent, and attn_tree_join
+// adds the parts in order, so results never depend on timing.
 #pragma once
 
 #include "common.cuh"
 
 namespace wide {
 
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTreeHD = 128;
 constexpr int kTreeMaxUnits = 4096;
 constexpr int kTreeMaxDraft = 1024;
@@ -32,13 +35,38 @@ struct TreeArgs {
     int n_seq, draft, n_q, n_kv, rep, Wt, Wh;
     int64_t cap, q_stride;
     float scale_log2;
-    // parts: slot 2 c (CTA c's first segment) and 2 c + 1
+    // parts: slot 2 c (a run begun in an earlier CTA than c) and 2 c + 1 (begun in c)
     float *part_o;                     // [2 n][rt][128]
     float2 *part_ml;                   // [2 n][rt] (max in log2 units, sum)
     int4 *joins;                       // [n]: run starting in CTA c: (last CTA, first slot, rows, 0); rows 0: none
     int32_t *join_rows;                // [n][rt] output row of each row of that run
     int32_t *status;
 };
+
+// 2^x by the SFU (results below the normal range become 0, which a weight in
+// bf16 next to one of at least 2^-8 loses anyway)
+__device__ __forceinline__ float exp2_sfu(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 16 bytes that are read once
+__device__ __forceinline__ uint4 load_stream(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
 
 // Sequence s: its earlier and new positions; both 0 if its lengths are bad.
 __device__ __forceinline__ int2 tree_lens(const TreeArgs &a, int s, bool report)
@@ -52,16 +80,36 @@ __device__ __forceinline__ int2 tree_lens(const TreeArgs &a, int s, bool report)
     return make_int2(cl, dl);
 }
 
-// cum[u] = blocks before unit u (u = s * n_kv + j; cum[U] = all), cnt[u] =
-// tokens that keep the group.  All threads of the CTA; ends with a barrier.
+// Places of one block of a run of `rows` rows.
+__host__ __device__ __forceinline__ int tree_weight(int rows) { return rows > 128 ? 2 : 1; }
+// Places of a unit of `rows` rows and nb blocks.
+__device__ __forceinline__ uint32_t tree_places(int rows, int rt, int nb, int rc)
+{
+    const int full = rows / rt, rest = rows - full * rt;
+    return nb ? (uint32_t)full * (uint32_t)(rc + tree_weight(rt) * nb) +
+                    (rest ? (uint32_t)(rc + tree_weight(rest) * nb) : 0u)
+              : 0u;
+}
+// CTAs that share `total` places: each has a block's worth at least, so every
+// CTA between a run's first and last has a part of it.
+__device__ __forceinline__ int tree_ctas(int grid, uint32_t total, int rt)
+{
+    const uint32_t most = total / (uint32_t)tree_weight(rt);
+    return (int)min((uint32_t)grid, most ? most : total);
+}
+
+// cum[u] = places before unit u (u = s * n_kv + j; cum[U] = all), cnt[u] =
+// tokens that keep the group; part: THREADS / 32 words of scratch, all in
+// shared memory.  All threads of the CTA; ends with a barrier.
 template <int THREADS>
-__device__ void tree_plan(const TreeArgs &a, int rt, int bk, uint32_t *cum, uint16_t *cnt)
+__device__ void tree_plan(const TreeArgs &a, int rt, int bk, int rc, uint32_t *cum, uint16_t *cnt,
+                          uint32_t *part)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int U = a.n_seq * a.n_kv;
     for (int s = warp; s < a.n_seq; s += THREADS / 32) {
         const int2 len = tree_lens(a, s, blockIdx.x == 0 && lane == 0);
-        const uint32_t nb = (uint32_t)((len.x + len.y + bk - 1) / bk);
+        const int nb = (len.x + len.y + bk - 1) / bk;
         for (int w = 0; w < (a.n_kv + 31) / 32; ++w) {
             const int nj = min(32, a.n_kv - 32 * w);
             int mine = 0;              // lane j: tokens that keep group 32 w + j
@@ -81,7 +129,7 @@ __device__ void tree_plan(const TreeArgs &a, int rt, int bk, uint32_t *cum, uint
             if (lane < nj) {
                 const int u = s * a.n_kv + 32 * w + lane;
                 cnt[u] = (uint16_t)mine;
-                cum[u + 1] = (uint32_t)((mine * a.rep + rt - 1) / rt) * nb;
+                cum[u + 1] = tree_places(mine * a.rep, rt, nb, rc);
             }
         }
     }
@@ -89,7 +137,6 @@ __device__ void tree_plan(const TreeArgs &a, int rt, int bk, uint32_t *cum, uint
         cum[0] = 0;
     __syncthreads();
     // inclusive scan of cum[1..U]: each thread a stretch, then the stretches
-    __shared__ uint32_t part[THREADS / 32];
     const int per = (U + THREADS - 1) / THREADS;
     const int lo = min(U, tid * per), hi = min(U, lo + per);
     uint32_t sum = 0;
@@ -115,7 +162,7 @@ __device__ void tree_plan(const TreeArgs &a, int rt, int bk, uint32_t *cum, uint
     __syncthreads();
 }
 
-// The unit that holds block b: the largest u with cum[u] <= b.
+// The unit that holds place b: the largest u with cum[u] <= b.
 __device__ __forceinline__ int tree_unit(const uint32_t *cum, int U, uint32_t b)
 {
     int lo = 0, hi = U;                // cum[lo] <= b < cum[hi]
@@ -129,7 +176,7 @@ __device__ __forceinline__ int tree_unit(const uint32_t *cum, int U, uint32_t b)
     return lo;
 }
 
-// Owner of block b when n CTAs share `total` blocks.
+// Owner of place b when n CTAs share `total`.
 __device__ __forceinline__ int tree_owner(uint32_t b, uint32_t total, int n)
 {
     return (int)((((uint64_t)b + 1) * (uint64_t)n - 1) / total);
@@ -137,8 +184,9 @@ __device__ __forceinline__ int tree_owner(uint32_t b, uint32_t total, int n)
 
 // Tokens of the unit that keep the group, numbers [from, to) of them, into
 // tok[]; by one whole warp.
+template <typename T>
 __device__ __forceinline__ void tree_tokens(const TreeArgs &a, int s, int j, int dl, int from,
-                                            int to, int32_t *tok)
+                                            int to, T *tok)
 {
     const int lane = threadIdx.x & 31;
     int seen = 0;
@@ -151,7 +199,7 @@ __device__ __forceinline__ void tree_tokens(const TreeArgs &a, int s, int j, int
         const uint32_t b = __ballot_sync(0xffffffffu, on);
         const int at = seen + __popc(b & ((1u << lane) - 1u));
         if (on && at >= from && at < to)
-            tok[at - from] = t;
+            tok[at - from] = (T)t;
         seen += __popc(b);
     }
 }
@@ -195,6 +243,9 @@ template <int THREADS> __device__ void tree_zero_skipped(const TreeArgs &a)
         }
     }
 }
+
+// attn_tree_tc.cu: runs of rt = 32, 64, 128 or 256 rows, by n CTAs.
+int attn_tree_tiles_launch(const TreeArgs &a, int kind, int rt, int n, cudaStream_t s);
 
 // Waits for the kernels this launch depends on (programmatic launch).
 __device__ __forceinline__ void grid_dependency_wait()

@@ -1,0 +1,1155 @@
+// attn_tree_tc.cu -- wide_attn_tree on the tensor cores: the rows of a run, up
+// to 256, share one pass over their keys.
+//
+// One persistent CTA per SM, 14 warps that hand work over through mbarriers:
+//   copy     one warp: tiles of 128 keys, then of their values, in turn, by
+//            TMA; bf16 straight into the operands' swizzled layout, 8-bit rows
+//            and their scales into a ring of raw tiles
+//   convert  8 warps (4 with two row halves): raw tiles to bf16 operand tiles,
+//            exactly, in a second ring.  A thread takes 32 codes with one
+//            scale; the bf16 pairs are bytes (0, 2) and (1, 3) of a word,
+//            which saves the permutes (integer instructions issue at half
+//            rate and are what bounds the conversion): the dims of an operand
+//            row are in the order 0 2 1 3 within each four, the queries are
+//            written in the same order and outputs put back at the end.  Values of new positions are checked:
+//            what is not finite is left out of the tile (0 * NaN would reach
+//            rows that do not attend it) and added to the attending rows at
+//            the end
+//   MMA      one thread:  S = Q K^T  (M 128 rows, N 128 keys)  and
+//            O += P V  (N 128 dims), fp32 in tensor memory; P, rounded to
+//            bf16, is read from tensor memory too
+//   softmax  4 warps per 128 rows.  A row's reference maximum moves only when
+//            it grows by more than 8 (log2 units), to a whole number, so weights
+//            stay within 2^8 and O is rarely rescaled; a tile's weights are computed with the
+//            reference so far and once more in the rare case that it moves.
+// Row layouts of a run (R copies of rt = 128 / R rows, or two halves):
+//   R = 1    a thread per row takes all 128 keys of a tile
+//   R = 2, 4 the rows are repeated R times along M and a thread takes 128 / R
+//            keys of the tile: the copies' weights for other keys are zero.  A
+//            softmax warp's exponentials are the longest step with few rows
+//            (16 keys a clock and SM, but 4 for one warp), and this spreads
+//            them over the SM's quarters.  The copies are added at the end.
+//   NM = 2   256 rows: two tiles of scores and outputs, whose softmax and
+//            MMAs overlap each other.
+// Tensor memory, 512 columns: scores 0-127 and 128-255 (two tiles in turn, or
+// one per half), outputs from 256 (and 384), weights from 384 and 448 (with
+// two halves: over the first columns of their scores).
+#include "attn_tree.cuh"
+#include "host.h"
+#include "kv.cuh"
+#include "umma.cuh"
+
+namespace wide {
+namespace {
+
+constexpr int kBK = 128;                         // keys per tile
+constexpr uint32_t kHalf = 128 * 128;            // 128 rows of 64 bf16, 128-byte swizzle
+constexpr uint32_t kTile = 2 * kHalf;            // 128 x 128 bf16
+constexpr uint32_t kRawCodes = kBK * kTreeHD;    // codes of a raw tile; the scales follow the ring
+constexpr uint32_t kRawScales = kBK * 4;
+constexpr int kRunCost = 3;                      // tiles' time that a run costs beside its tiles
+constexpr int kOPitch = kTreeHD + 4;             // floats; row pitch when copies are added
+
+template <int KIND, int NM> struct Cfg {
+    static constexpr bool k8 = KIND != WIDE_KV_BF16;
+    // warps, and registers per thread: every four warps the same number, out of
+    // kLaunchRegs each (setmaxnreg); the last of the issuing four idles
+    static constexpr int kSoftWarps = 4 * NM, kConvWarps = !k8 ? 4 : NM == 2 ? 8 : 16;
+    static constexpr int kMmaWarp = kSoftWarps + kConvWarps, kCopyWarp = kMmaWarp + 1;
+    static constexpr int kWarps = kMmaWarp + 4, kThreads = 32 * kWarps;
+    static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+    static constexpr int kConvRegs = k8 ? (NM == 2 ? 72 : 64) : 72;
+    static constexpr int kIssueRegs = k8 && NM == 1 ? 56 : 72;
+    static constexpr int kSoftRegs =
+        (kLaunchRegs * kWarps - kConvRegs * kConvWarps - kIssueRegs * 4) / kSoftWarps / 8 * 8 > 232
+            ? 232
+            : (kLaunchRegs * kWarps - kConvRegs * kConvWarps - kIssueRegs * 4) / kSoftWarps / 8 * 8;
+    static_assert(kSoftRegs >= kLaunchRegs && kConvRegs <= kLaunchRegs && kIssueRegs <= kLaunchRegs, "registers");
+    static constexpr int kOps = k8 ? 5 - NM : 7 - NM;      // operand tiles
+    static constexpr int kRaw = k8 ? 5 - NM : 1;           // raw tiles (bf16: unused)
+    static constexpr uint32_t kOffOps = NM * kTile, kOffRaw = kOffOps + kOps * kTile;
+    static constexpr uint32_t kOffScales = kOffRaw + (k8 ? kRaw * kRawCodes : 0);
+    static constexpr uint32_t kOffCtl = kOffScales + (k8 ? kRaw * kRawScales : 0);
+};
+
+// One run, as far as a CTA does it.
+struct Run {
+    int64_t row0;                // the unit's first cache row
+    int s, j, cl, dl;            // sequence, KV head, earlier and new positions
+    int run, blk0, nt;           // number within the unit, first tile, tiles
+    int nrows, nm, slot;         // rows, row halves in use, workspace slot
+    int whole;                   // all of the run's tiles
+};
+
+template <int OPS, int RAW, int ROWS> struct __align__(16) TcCtl {
+    uint64_t op_full[OPS];                       // bf16: the tile's copies have landed
+    uint64_t op_ready[OPS];                      // the convert warps are done with the tile
+    uint64_t op_empty[OPS];                      // the MMAs have read it
+    uint64_t raw_full[RAW], raw_empty[RAW];      // raw rows landed / converted
+    uint64_t q_full;                             // the run's queries are written
+    uint64_t s_full[2];                          // scores: of a row half, or of even / odd tiles
+    // (a buffer each, as the scores: a softmax warp may be a tile ahead of another)
+    uint64_t p_full[2];                          // the weights are written (4 warps)
+    uint64_t pv_done[2];                         // O += P V is complete
+    uint64_t all_done;                           // error path: every MMA is complete
+    Run run;                                     // the current one; nt 0: there are no more
+    uint32_t tmem;
+    int abort, any_bad;
+    uint32_t first;                              // the plan: this CTA's places and the first's unit
+    uint32_t end, total;
+    int u0;
+    uint32_t base;
+    int16_t tok[ROWS], list[ROWS];               // token of each row, -1: none; tokens of the next run
+    uint32_t bad[kTreeMaxDraft / 32];            // new positions with a value that is not finite
+};
+
+// Waits for this thread's tensor memory loads; v, loaded by one of them, is
+// not used before.
+__device__ __forceinline__ void tmem_ld_wait_for(float (&v)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                   "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]),
+                   "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
+                   "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+                   "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29])
+                 :: "memory");
+    // (an asm statement takes 30 operands at most)
+    asm volatile("" : "+f"(v[30]), "+f"(v[31])::"memory");
+}
+
+// a * b + c and a + b of pairs, each element rounded as fmaf / + does
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 32 words of this thread's lane.
+__device__ __forceinline__ void tmem_ld32w(uint32_t taddr, uint32_t *w)
+{
+    float v[32];
+    umma::tmem_ld32(taddr, v);
+    tmem_ld_wait_for(v);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        w[e] = __float_as_uint(v[e]);
+}
+
+// Weights 2^(sc x - mref) of COLS scores x in tensor memory as bf16 pairs;
+// returns the largest sc x and the sum of the weights.  TAIL: see(i) has the
+// bits of the scores 32 i .. that the row attends.
+template <int COLS, bool TAIL, class See>
+__device__ __forceinline__ float2 tile_weights(uint32_t ts, float sc, float mref, uint32_t (&pw)[COLS / 2],
+                                               See &&see)
+{
+    const float mb = mref > -INFINITY ? -mref : 0.f;
+    const float2 sc2 = make_float2(sc, sc), mb2 = make_float2(mb, mb);
+    float mx[2] = {-INFINITY, -INFINITY};
+    float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int i = 0; i < COLS / 32; ++i) {
+        float v[32];
+        umma::tmem_ld32(ts + 32 * i, v);
+        tmem_ld_wait_for(v);
+        if (TAIL) {
+            const uint32_t bits = see(i);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                v[e] = (bits >> e) & 1u ? v[e] : -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+            mx[(e >> 1) & 1] = max3(mx[(e >> 1) & 1], v[e], v[e + 1]);
+            const float2 x = fma2(make_float2(v[e], v[e + 1]), sc2, mb2);
+            const float2 p = make_float2(exp2_sfu(x.x), exp2_sfu(x.y));
+            ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], p);
+            pw[i * 16 + e / 2] = pack_bf16(p.x, p.y);
+        }
+    }
+    ls[0] = add2(ls[0], ls[1]);
+    return make_float2(fmaxf(mx[0], mx[1]) * sc, ls[0].x + ls[0].y);
+}
+
+// Position in a ring of N slots.
+template <int N> struct Ring {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void next(int by = 1)
+    {
+        slot += (uint32_t)by;
+        if (slot >= N) {
+            slot -= N;
+            phase ^= 1u;
+        }
+    }
+};
+
+// A bounded wait: gives up after kPolls polls (each waits some tens of
+// nanoseconds in the hardware), or when another warp has.
+constexpr uint32_t kPolls = 1u << 25;
+__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int *abort, int32_t *status)
+{
+#pragma unroll 1
+    for (uint32_t n = 0; !mbar_try_wait(bar, parity); ++n) {
+        if ((n & 1023u) != 1023u)
+            continue;
+        if (*(volatile int *)abort)
+            return false;
+        if (n >= kPolls) {
+            set_status(status, WIDE_DEV_TIMEOUT);
+            *(volatile int *)abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A's rows are lanes, two bf16 per column.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// True in one thread of a whole warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+template <int N> __device__ __forceinline__ void more_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void fewer_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 16 words to 16 columns of this thread's lane.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *w)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]),
+        "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
+        : "memory");
+}
+
+// 4 bytes, or zeros if !in (src must still be a valid address).
+__device__ __forceinline__ void cp_async4_zfill(uint32_t dst, const void *src, bool in)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(in ? 4 : 0)
+                 : "memory");
+}
+
+// Takes what is not finite out of 8 bf16; whether there was any.
+__device__ __forceinline__ bool drop_not_finite(uint4 &w)
+{
+    uint32_t *x = reinterpret_cast<uint32_t *>(&w);
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if ((x[e] & 0x7f80u) == 0x7f80u) {
+            x[e] &= 0xffff0000u;
+            bad = true;
+        }
+        if ((x[e] & 0x7f800000u) == 0x7f800000u) {
+            x[e] &= 0x0000ffffu;
+            bad = true;
+        }
+    }
+    return bad;
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+
+// 32 codes with one scale byte as bf16 to 64 bytes of a swizzled operand row;
+// dst: address of the first 16 (the next ones differ in bits 4 and 5).
+template <int KIND>
+__device__ __forceinline__ void convert32(uint32_t dst, const uint4 c0, const uint4 c1, uint32_t sc)
+{
+    const uint32_t m = kv_mult<KIND>(sc) * 0x00010001u;
+    uint32_t o[16];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t x = word(e < 4 ? c0 : c1, e & 3);
+        kv_pairs_0213<KIND>(x, m, o[2 * e], o[2 * e + 1]);
+    }
+    if (KIND == WIDE_KV_E4M3 && sc > 134u && sc < 255u) {
+        const uint32_t mh = kv_mult_high(sc) * 0x00010001u;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            o[e] = mul_bf16x2(o[e], mh);
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+        st_shared16(dst ^ (uint32_t)(g << 4), o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
+}
+
+// The bits of row `t` for the 32 positions from kb on: earlier positions all,
+// new ones as the tree says, none past the end.
+__device__ __forceinline__ uint32_t seen_bits(const TreeArgs &a, int s, int t, int kb, int cl, int dl)
+{
+    auto low = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+    const uint32_t ctx = low(cl - kb), end = low(cl + dl - kb);
+    uint32_t tree;
+    if (t < 0) {
+        tree = 0u;
+    } else if (!a.tree) {
+        tree = low(cl + t + 1 - kb);
+    } else {
+        const uint32_t *w = a.tree + ((size_t)s * a.draft + t) * a.Wt;
+        const int j0 = kb - cl;                   // new position of bit 0
+        const int i0 = j0 >> 5, sh = j0 & 31;     // floor division
+        const uint32_t lo = i0 >= 0 && i0 < a.Wt ? w[i0] : 0u;
+        const uint32_t hi = i0 + 1 >= 0 && i0 + 1 < a.Wt ? w[i0 + 1] : 0u;
+        tree = __funnelshift_r(lo, hi, sh);
+    }
+    return (ctx | tree) & end;
+}
+
+template <int KIND, int NM, int R>
+__global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
+    attn_tree_tiles(const TreeArgs a, const __grid_constant__ CUtensorMap map_k,
+                    const __grid_constant__ CUtensorMap map_v)
+{
+    using C = Cfg<KIND, NM>;
+    constexpr int kThreads = C::kThreads, kWarps = C::kWarps, kMmaWarp = C::kMmaWarp, kCopyWarp = C::kCopyWarp,
+                  kPlanWarp = C::kMmaWarp + 2;
+    constexpr int rt = NM == 2 ? 256 : 128 / R;       // rows of a run
+    constexpr int kCols = 128 / R;                    // keys of a tile per softmax thread
+    using Ctl = TcCtl<C::kOps, C::kRaw, rt>;
+    static_assert(C::kOffCtl + sizeof(Ctl) <= 227 * 1024, "shared memory");
+    static_assert(128 * (kOPitch * 4 + 8) <= C::kOps * kTile, "the copies' outputs fit in the ring");
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int me = (int)blockIdx.x, U = a.n_seq * a.n_kv;
+    if (smem_u32(smem) & 1023u) {
+        if (tid == 0) {
+            set_status(a.status, WIDE_DEV_LAYOUT);
+            a.joins[me] = make_int4(0, 0, 0, 0);
+        }
+        return;
+    }
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + C::kOffCtl);
+    uint8_t *ops = smem + C::kOffOps, *raw = smem + C::kOffRaw;
+
+    // ---- the plan, in the ring of operand tiles
+    {
+        uint32_t *cum = reinterpret_cast<uint32_t *>(ops);
+        uint16_t *cnt = reinterpret_cast<uint16_t *>(cum + kTreeMaxUnits + 1);
+        uint32_t *part = reinterpret_cast<uint32_t *>(cnt + kTreeMaxUnits + 2);
+        static_assert((kTreeMaxUnits + 1) * 4 + (kTreeMaxUnits + 2) * 2 + kWarps * 4 <= C::kOps * kTile,
+                      "the plan fits in the ring");
+        tree_plan<kThreads>(a, rt, kBK, kRunCost, cum, cnt, part);
+        const uint32_t total = cum[U];
+        const int n_cta = tree_ctas((int)gridDim.x, total, rt);
+        if (me >= n_cta) {
+            if (tid == 0)
+                a.joins[me] = make_int4(0, 0, 0, 0);
+            tree_zero_skipped<kThreads>(a);
+            return;
+        }
+        if (tid == 0) {
+            ctl->abort = 0;
+            ctl->total = total;
+            ctl->first = (uint32_t)((uint64_t)me * total / n_cta);
+            ctl->end = (uint32_t)((uint64_t)(me + 1) * total / n_cta);
+            ctl->u0 = tree_unit(cum, U, ctl->first);
+            ctl->base = cum[ctl->u0];
+            for (int i = 0; i < C::kOps; ++i) {
+                mbar_init(&ctl->op_full[i], 1);
+                mbar_init(&ctl->op_ready[i], C::kConvWarps);
+                mbar_init(&ctl->op_empty[i], 1);
+            }
+            for (int i = 0; i < C::kRaw; ++i) {
+                mbar_init(&ctl->raw_full[i], 33);
+                mbar_init(&ctl->raw_empty[i], C::kConvWarps);
+            }
+            mbar_init(&ctl->q_full, C::kConvWarps);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&ctl->s_full[i], 1);
+                mbar_init(&ctl->p_full[i], 4);
+                mbar_init(&ctl->pv_done[i], 1);
+            }
+            mbar_init(&ctl->all_done, 1);
+            fence_mbar_init();
+        }
+    }
+    if (warp == kMmaWarp) {
+        umma::tmem_alloc(&ctl->tmem, 512);
+        umma::tmem_relinquish();
+    }
+    if (tid == 32 * kCopyWarp) {
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+    }
+    fence_proxy_async_smem();                         // the ring is written by copies next
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tmem = ctl->tmem;
+    const uint32_t t_o = tmem + 256, t_p = NM == 2 ? tmem : tmem + 384;
+    constexpr uint32_t p_step = NM == 2 ? 128 : 64;   // columns from one weights buffer to the next
+
+    // ring positions and parities that a role carries from run to run
+    Ring<C::kRaw> raw_at;
+    Ring<C::kOps> op_at;
+    uint32_t q_phase = 0;
+    // bit b: parity of the tiles that buffer b has held, and with it of the
+    // completions so far of s_full[b], p_full[b] and pv_done[b]
+    uint32_t held = 0;
+    bool ok = true;
+    const float sc = a.scale_log2;
+    int *abort = &ctl->abort;
+
+    // The runs of this CTA's places, one after another: each role calls it with
+    // its part of the work.  All threads meet before and after a run.
+    const Run &x = ctl->run;
+    auto each_run = [&](auto &&work) {
+        for (;;) {
+            __syncthreads();
+            if (x.nt == 0)
+                break;
+            work();
+            const int nt = x.nt;
+            held ^= x.nm == 2 ? (nt & 1) * 3u : (((nt + 1) >> 1) & 1u) | ((nt >> 1) & 1u) << 1;
+            if (__syncthreads_or(!ok))
+                break;
+        }
+        umma::fence_before_sync();
+        __syncthreads();
+    };
+
+    // -------------------------------------------------------------- plan
+    // One warp finds the next run and its tokens while the others work on the
+    // current one.  Lane i holds the places before unit u0 + i and after it,
+    // and its tokens.
+    auto plan_role = [&] {
+        const uint32_t total = ctl->total, end = ctl->end;
+        const int n_cta = tree_ctas((int)gridDim.x, total, rt);
+        int u0 = ctl->u0;
+        uint32_t b = ctl->first, base = ctl->base, upto = 0;
+        int mine = 0;
+        int4 join = make_int4(0, 0, 0, 0);
+        auto window = [&] {                           // of the 32 units from u0 on, `base` places before them
+            const int u = u0 + lane, s = min(u, U - 1) / a.n_kv, j = u - s * a.n_kv;
+            const int2 len = u < U ? tree_lens(a, s, false) : make_int2(0, 0);
+            mine = a.heads ? 0 : len.y;
+            if (a.heads)
+                for (int t = 0; t < len.y; ++t)
+                    mine += (a.heads[((size_t)s * a.draft + t) * a.Wh + (j >> 5)] >> (j & 31)) & 1u;
+            upto = tree_places(mine * a.rep, rt, (len.x + len.y + kBK - 1) / kBK, kRunCost);
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t o = __shfl_up_sync(0xffffffffu, upto, off);
+                upto += lane >= off ? o : 0u;
+            }
+            upto += base;
+        };
+        auto next = [&](Run &r) {                     // false: none left
+            for (;;) {
+                r.nt = 0;
+                if (b >= end)
+                    return false;
+                uint32_t past = __ballot_sync(0xffffffffu, upto <= b);
+                while (past == 0xffffffffu) {
+                    base = __shfl_sync(0xffffffffu, upto, 31);
+                    u0 += 32;
+                    window();
+                    past = __ballot_sync(0xffffffffu, upto <= b);
+                }
+                const int i = __popc(past), u = u0 + i;    // upto rises with the lane
+                const uint32_t before = i ? __shfl_sync(0xffffffffu, upto, i - 1) : base;
+                r.s = u / a.n_kv;
+                r.j = u - r.s * a.n_kv;
+                const int2 len = tree_lens(a, r.s, false);
+                r.cl = len.x;
+                r.dl = len.y;
+                const int nb = (r.cl + r.dl + kBK - 1) / kBK, per = kRunCost + tree_weight(rt) * nb;
+                const int rows = __shfl_sync(0xffffffffu, mine, i) * a.rep;
+                r.run = min((int)(b - before) / per, (rows - 1) / rt);
+                const uint32_t run0 = before + (uint32_t)r.run * per;   // the run's first place
+                r.nrows = min(rt, rows - r.run * rt);
+                const int w = tree_weight(r.nrows), pos = (int)(b - run0);
+                const int stop = (int)min((uint32_t)(kRunCost + w * nb), (uint32_t)pos + (end - b));
+                b += (uint32_t)(stop - pos);
+                r.blk0 = (max(pos - kRunCost, 0) + w - 1) / w;
+                r.nt = (max(stop - kRunCost, 0) + w - 1) / w - r.blk0;
+                if (r.nt == 0)
+                    continue;
+                r.nm = NM == 2 ? w : 1;
+                r.whole = r.nt == nb;
+                r.slot = 2 * me + (r.blk0 == 0);
+                r.row0 = (int64_t)u * a.cap;
+                if (!r.whole && r.blk0 == 0)          // the run starts here: record its extent
+                    join = make_int4(tree_owner(run0 + (uint32_t)(kRunCost + w * (nb - 1)), total, n_cta),
+                                     r.slot, r.nrows, 0);
+                tree_tokens(a, r.s, r.j, r.dl, r.run * rt / a.rep, (r.run * rt + r.nrows - 1) / a.rep + 1,
+                            ctl->list);
+                __syncwarp();
+                return true;
+            }
+        };
+        window();
+        Run r;
+        bool more = next(r);
+        for (;;) {
+            if (lane == 0) {
+                ctl->run = r;
+                ctl->any_bad = 0;
+            }
+            ctl->bad[lane] = 0;
+            if (more) {
+                const int lo = r.run * rt / a.rep;
+                for (int i = lane; i < rt; i += 32)
+                    ctl->tok[i] = i < r.nrows ? ctl->list[(r.run * rt + i) / a.rep - lo] : (int16_t)-1;
+            }
+            __syncthreads();
+            if (!more)
+                break;
+            more = next(r);
+            if (__syncthreads_or(0)) {
+                join = make_int4(0, 0, 0, 0);
+                break;
+            }
+        }
+        if (lane == 0)
+            a.joins[me] = join;
+        umma::fence_before_sync();
+        __syncthreads();
+    };
+
+    // -------------------------------------------------------------- copy
+    auto copy_role = [&] {
+        const int blk0 = x.blk0, nt = x.nt, cl = x.cl, dl = x.dl;
+        const int64_t row0 = x.row0;
+        const int nkeys = cl + dl;
+        if constexpr (C::k8) {
+            uint32_t issued = 0;
+            for (int i = 0; i < 2 * nt; ++i) {
+                const int p0 = (blk0 + (i >> 1)) * kBK;
+                ok = __all_sync(0xffffffffu, tc_wait(&ctl->raw_empty[raw_at.slot], raw_at.phase ^ 1u,
+                                                     abort, a.status));
+                if (!ok)
+                    break;
+                uint64_t *bar = &ctl->raw_full[raw_at.slot];
+                if (lane == 0) {
+                    // (rows past the unit's end may hold anything: finite with scale 0)
+                    mbar_arrive_expect_tx(bar, kRawCodes);
+                    tma_load_2d(raw + raw_at.slot * kRawCodes, i & 1 ? &map_v : &map_k, 0,
+                                (int32_t)(row0 + p0), bar);
+                }
+                const uint8_t *scales = (i & 1 ? a.vs : a.ks) + (row0 + p0) * 4;
+                const uint32_t dst = smem_u32(smem + C::kOffScales + raw_at.slot * kRawScales);
+#pragma unroll
+                for (int r = lane; r < kBK; r += 32) {
+                    const bool in = p0 + r < nkeys;
+                    cp_async4_zfill(dst + r * 4, scales + (in ? r * 4 : 0), in);
+                }
+                cp_async_arrive_noinc(bar);
+                raw_at.next();
+                ++issued;
+            }
+            if (!ok) {                             // copies in flight land before shared memory goes
+                cp_async_wait_all();
+                Ring<C::kRaw> at = raw_at;
+                for (uint32_t i = 0; i < min(issued, (uint32_t)C::kRaw); ++i) {
+                    at.phase ^= at.slot == 0;
+                    at.slot = at.slot == 0 ? C::kRaw - 1 : at.slot - 1;
+                    mbar_wait(&ctl->raw_full[at.slot], at.phase);
+                }
+            }
+        } else if (lane == 0) {
+            uint32_t issued = 0;
+            for (int i = 0; i < 2 * nt; ++i) {
+                ok = tc_wait(&ctl->op_empty[op_at.slot], op_at.phase ^ 1u, abort, a.status);
+                if (!ok)
+                    break;
+                uint64_t *bar = &ctl->op_full[op_at.slot];
+                uint8_t *dst = ops + op_at.slot * kTile;
+                const int32_t y = (int32_t)(row0 + (int64_t)(blk0 + (i >> 1)) * kBK);
+                mbar_arrive_expect_tx(bar, kTile);
+                tma_load_2d(dst, i & 1 ? &map_v : &map_k, 0, y, bar);
+                tma_load_2d(dst + kHalf, i & 1 ? &map_v : &map_k, 64, y, bar);
+                op_at.next();
+                ++issued;
+            }
+            if (!ok) {
+                Ring<C::kOps> at = op_at;
+                for (uint32_t i = 0; i < min(issued, (uint32_t)C::kOps); ++i) {
+                    at.phase ^= at.slot == 0;
+                    at.slot = at.slot == 0 ? C::kOps - 1 : at.slot - 1;
+                    mbar_wait(&ctl->op_full[at.slot], at.phase);
+                }
+            }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+    };
+
+    // ----------------------------------------------------------- convert
+    auto convert_role = [&] {
+        const int &s = x.s, &j = x.j, &run = x.run, &nm = x.nm;
+        const int cl = x.cl, dl = x.dl, blk0 = x.blk0, nt = x.nt;
+        constexpr int kConv = 32 * C::kConvWarps;
+        const int ct = tid - 32 * C::kSoftWarps;
+        // (8 bits) this thread's row of a tile, its swizzle pattern, and its first block of 32
+        const int row = ct & 127, blk = ct >> 7;
+        const uint32_t row_swz = swz128(row, 0);
+        // the queries first
+        for (int i = ct; i < nm * 128 * 16; i += kConv) {
+            const int r = i >> 4, c = i & 15, q_row = NM == 2 ? r : r % rt, tok = ctl->tok[q_row];
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (tok >= 0)
+                w = *reinterpret_cast<const uint4 *>(
+                    a.q + ((int64_t)s * a.draft + tok) * a.q_stride +
+                    (int64_t)(j * a.rep + (run * rt + q_row) % a.rep) * kTreeHD + c * 8);
+            if (C::k8)                                // dims in the operand order 0 2 1 3
+                w = make_uint4(__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632),
+                               __byte_perm(w.z, w.w, 0x5410), __byte_perm(w.z, w.w, 0x7632));
+            *reinterpret_cast<uint4 *>(smem + (r >> 7) * kTile + (c >> 3) * kHalf +
+                                       swz128(r & 127, c & 7)) = w;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&ctl->q_full);
+        auto note_bad = [&](int jj) {
+            if (jj < dl) {
+                atomicOr(&ctl->bad[jj >> 5], 1u << (jj & 31));
+                ctl->any_bad = 1;
+            }
+        };
+        for (int i = 0; i < 2 * nt && ok; ++i) {
+            const int p0 = (blk0 + (i >> 1)) * kBK;
+            const bool fresh = (i & 1) && p0 + kBK > cl;    // values with new positions
+            uint8_t *tile = ops + op_at.slot * kTile;
+            if constexpr (C::k8) {
+                constexpr int kN = kBK * 4 / kConv;             // blocks of 32 codes of a thread
+                ok = tc_wait(&ctl->raw_full[raw_at.slot], raw_at.phase, abort, a.status) &&
+                     tc_wait(&ctl->op_empty[op_at.slot], op_at.phase ^ 1u, abort, a.status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                uint32_t sb4 = reinterpret_cast<const uint32_t *>(smem + C::kOffScales + raw_at.slot * kRawScales)[row];
+                if (fresh && p0 + row >= cl && __vcmpeq4(sb4, ~0u)) {   // their codes are zeros
+                    note_bad(p0 + row - cl);
+                    sb4 &= ~__vcmpeq4(sb4, ~0u);
+                }
+                const uint32_t from = smem_u32(raw) + raw_at.slot * kRawCodes + row_swz;
+                const uint32_t to = smem_u32(ops) + op_at.slot * kTile + row_swz;
+#pragma unroll
+                for (int n = 0; n < kN; ++n) {
+                    const int bk = blk + n * (kConv / 128);     // pieces 2 bk, 2 bk + 1 of the codes' row
+                    const uint32_t f = from ^ (uint32_t)(bk << 5);
+                    convert32<KIND>((to ^ (uint32_t)((bk & 1) << 6)) + (uint32_t)(bk >> 1) * kHalf,
+                                    ld_shared16(f), ld_shared16(f ^ 16u), (sb4 >> (8 * bk)) & 255u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&ctl->raw_empty[raw_at.slot]);
+                    mbar_arrive(&ctl->op_ready[op_at.slot]);
+                }
+                raw_at.next();
+            } else {
+                ok = __all_sync(0xffffffffu, tc_wait(&ctl->op_full[op_at.slot], op_at.phase,
+                                                     abort, a.status));
+                if (ok && fresh) {
+                    // rows of new positions, and rows past the end, which may hold anything
+                    for (int x = max(cl - p0, 0) * 16 + ct; x < kBK * 16; x += kConv) {
+                        const int r = x >> 4, c = x & 15;
+                        uint4 *at = reinterpret_cast<uint4 *>(tile + (c >> 3) * kHalf + swz128(r, c & 7));
+                        uint4 w = *at;
+                        if (drop_not_finite(w)) {
+                            *at = w;
+                            note_bad(p0 + r - cl);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (ok && lane == 0)
+                    mbar_arrive(&ctl->op_ready[op_at.slot]);
+            }
+            op_at.next();
+        }
+    };
+
+    // --------------------------------------------------------------- MMA
+    // The whole warp walks through the tiles and one thread issues: with values
+    // that are the same in all lanes the operands stay in uniform registers.
+    // (Issued from a branch of one lane, eight MMAs took 700 clocks.)
+    auto mma_role = [&] {
+        const int nt = __shfl_sync(0xffffffffu, x.nt, 0);
+        const bool two = NM == 2 && __shfl_sync(0xffffffffu, x.nm, 0) == 2;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t tm_p = NM == 2 ? tm : tm + 384;
+        constexpr uint32_t idesc_s = umma::idesc_bf16_f32(128, 128);
+        constexpr uint32_t idesc_pv = umma::idesc_bf16_f32_bmn(128, 128);
+        Ring<C::kOps> k_at = op_at, v_at = op_at;
+        v_at.next();
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, tc_wait(bar, parity, abort, a.status));
+        };
+        auto ready = [&](const Ring<C::kOps> &at) {
+            return (C::k8 || wait(&ctl->op_full[at.slot], at.phase)) && wait(&ctl->op_ready[at.slot], at.phase);
+        };
+        // scores of tile t for row half m; the keys' slot is free after the last half
+        auto scores = [&](int t, int m, bool last) {
+            const uint32_t buf = two ? m : t & 1;
+            const uint64_t q0 = umma::desc_kmajor_sw128(smem_u32(smem) + (uint32_t)m * kTile);
+            const uint64_t k0 = umma::desc_kmajor_sw128(smem_u32(ops) + k_at.slot * kTile);
+            umma::fence_after_sync();
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kTreeHD / 16; ++k) {
+                    const uint32_t off = ((uint32_t)(k >> 2) * kHalf + (uint32_t)(k & 3) * 32u) >> 4;
+                    umma::mma_bf16(tm + buf * 128u, q0 + off, k0 + off, idesc_s, k != 0);
+                }
+                umma::commit(&ctl->s_full[buf]);
+                if (last)
+                    umma::commit(&ctl->op_empty[k_at.slot]);
+            }
+            __syncwarp();
+            if (last)
+                k_at.next(2);
+        };
+        // O += P V of tile t for row half m
+        auto product = [&](int t, int m, bool last) {
+            const uint32_t buf = two ? m : t & 1;
+            const uint64_t v0 = umma::desc_mnmajor_sw128(smem_u32(ops) + v_at.slot * kTile, kHalf);
+            umma::fence_after_sync();
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kBK / 16; ++k)
+                    mma_bf16_ta(tm + 256u + (uint32_t)m * 128u, tm_p + buf * p_step + (uint32_t)k * 8u,
+                                v0 + (uint32_t)k * (16u * 128u >> 4), idesc_pv, (t | k) != 0);
+                umma::commit(&ctl->pv_done[buf]);
+                if (last)
+                    umma::commit(&ctl->op_empty[v_at.slot]);
+            }
+            __syncwarp();
+            if (last)
+                v_at.next(2);
+        };
+        auto weights_ready = [&](int t, int m) {
+            const uint32_t buf = two ? m : t & 1;
+            return wait(&ctl->p_full[buf], ((held >> buf) + (uint32_t)(two ? t : t >> 1)) & 1u);
+        };
+        ok = wait(&ctl->q_full, q_phase) && ready(k_at);
+        if (two) {
+            if (ok) {
+                scores(0, 0, false);
+                scores(0, 1, true);
+            }
+            for (int t = 0; t < nt && ok; ++t) {
+                const bool more = t + 1 < nt;
+                ok = weights_ready(t, 0) && ready(v_at);
+                if (!ok)
+                    break;
+                product(t, 0, false);
+                if (more) {                           // after the product that reads the weights
+                    ok = ready(k_at);
+                    if (!ok)
+                        break;
+                    scores(t + 1, 0, false);
+                }
+                ok = weights_ready(t, 1);
+                if (!ok)
+                    break;
+                product(t, 1, true);
+                if (more)
+                    scores(t + 1, 1, true);
+            }
+        } else {
+            if (ok)
+                scores(0, 0, true);
+            for (int t = 0; t < nt && ok; ++t) {
+                if (t + 1 < nt) {
+                    ok = ready(k_at);
+                    if (!ok)
+                        break;
+                    scores(t + 1, 0, true);
+                }
+                ok = weights_ready(t, 0) && ready(v_at);
+                if (!ok)
+                    break;
+                product(t, 0, true);
+            }
+        }
+        if (!ok) {
+            // every MMA issued so far completes before tensor memory is freed
+            if (elect_one())
+                umma::commit(&ctl->all_done);
+            __syncwarp();
+            mbar_wait(&ctl->all_done, 0);
+        }
+        op_at = k_at;
+        q_phase ^= 1u;
+    };
+
+    // ----------------------------------------------------------- softmax
+    auto softmax_role = [&] {
+        // (references: loaded from shared memory where they are used, not held in registers)
+        const int &s = x.s, &j = x.j, &dl = x.dl, &run = x.run, &nrows = x.nrows, &slot = x.slot, &whole = x.whole;
+        const int64_t &row0 = x.row0;
+        const int cl = x.cl, blk0 = x.blk0, nt = x.nt;
+        if ((warp >> 2) >= x.nm)
+            return;
+        const int m = warp >> 2, quad = warp & 3;
+        const int r = NM == 2 ? tid : tid % rt;               // row of the run
+        const int c0 = NM == 2 ? 0 : tid / rt * kCols;        // first key of the tile
+        const uint32_t lanes = (uint32_t)quad << 21;
+        const uint32_t to = t_o + (uint32_t)m * 128u + lanes;
+        const int tok = ctl->tok[r];
+        const bool any = (NM == 2 ? warp * 32 : (quad * 32) % rt) < nrows;   // a live row in this warp
+        float mref = -INFINITY, l = 0.f;
+        const bool two = x.nm == 2;
+        for (int t = 0; t < nt; ++t) {
+            const int buf = two ? m : t & 1;
+            const uint32_t par = (held >> buf) + (uint32_t)(two ? t : t >> 1);
+            ok = tc_wait(&ctl->s_full[buf], par & 1u, abort, a.status);
+            // the buffer's last weights are read (complete already: the scores came after)
+            if (two ? t > 0 : t > 1)
+                ok = ok && tc_wait(&ctl->pv_done[buf], (par + 1u) & 1u, abort, a.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                break;
+            umma::fence_after_sync();
+            if (any) {
+                const uint32_t ts = tmem + (uint32_t)buf * 128u + lanes + (uint32_t)c0;
+                const int k0 = (blk0 + t) * kBK + c0;
+                const uint32_t tp = t_p + (uint32_t)buf * p_step + lanes + (uint32_t)(c0 / 2);
+                float alpha = 1.f;
+                // up to 64 keys at a time: their weights with the reference maximum so far, and
+                // once more if it moves
+                constexpr int kStep = kCols < 64 ? kCols : 64;
+#pragma unroll 1
+                for (int h = 0; h < kCols / kStep; ++h) {
+                    uint32_t pw[kStep / 2];
+                    float2 w;
+                    float up_by = 1.f;
+                    const int kh = k0 + h * kStep;
+#pragma unroll 1
+                    for (int pass = 0;; ++pass) {
+                        if (kh + kStep > cl)
+                            w = tile_weights<kStep, true>(ts + h * kStep, sc, mref, pw, [&](int i) {
+                                return seen_bits(a, s, tok, kh + 32 * i, cl, dl);
+                            });
+                        else
+                            w = tile_weights<kStep, false>(ts + h * kStep, sc, mref, pw, [](int) { return 0u; });
+                        const bool up = w.x > mref + 8.f;
+                        if (pass || !__any_sync(0xffffffffu, up))
+                            break;
+                        if (up) {
+                            // a whole number (of log2 units), so that scaling by the step is exact
+                            const float m1 = ceilf(w.x);
+                            up_by = m1 - mref <= 126.f ? exp2i((int)(mref - m1)) : 0.f;
+                            mref = m1;
+                        }
+                    }
+                    l = l * up_by + w.y;
+                    alpha *= up_by;
+                    if (h && __any_sync(0xffffffffu, up_by != 1.f)) {   // the weights stored before
+                        uint32_t y[kStep / 2];
+                        tmem_ld32w(tp, y);
+                        const uint32_t f = pack_bf16(up_by, up_by);
+#pragma unroll
+                        for (int e = 0; e < kStep / 2; ++e)
+                            y[e] = mul_bf16x2(y[e], f);
+#pragma unroll
+                        for (int i = 0; i < kStep / 32; ++i)
+                            tmem_st16(tp + 16 * i, y + 16 * i);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kStep / 32; ++i)
+                        tmem_st16(tp + h * (kStep / 2) + 16 * i, pw + 16 * i);
+                    umma::tmem_st_wait();
+                }
+                if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    if (!two) {                        // the product before must be complete
+                        ok = __all_sync(0xffffffffu, tc_wait(&ctl->pv_done[buf ^ 1],
+                                                             ((held >> (buf ^ 1)) + (uint32_t)((t - 1) >> 1)) & 1u,
+                                                             abort, a.status));
+                        if (!ok)
+                            break;
+                        umma::fence_after_sync();
+                    }
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        float o[32];
+                        umma::tmem_ld32(to + 32 * i, o);
+                        tmem_ld_wait_for(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] *= alpha;
+                        umma::tmem_st32(to + 32 * i, o);
+                    }
+                    umma::tmem_st_wait();
+                }
+            }
+            umma::fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&ctl->p_full[buf]);
+        }
+        if (ok) {
+            const int t = nt - 1, buf = two ? m : t & 1;
+            ok = __all_sync(0xffffffffu, tc_wait(&ctl->pv_done[buf],
+                                                 ((held >> buf) + (uint32_t)(two ? t : t >> 1)) & 1u,
+                                                 abort, a.status));
+        }
+        if (ok) {
+            umma::fence_after_sync();
+            // what is not finite in the new positions that the row of token row_tok attends, added
+            // to its elements d ..
+            auto add_bad = [&](int row_tok, int d, auto &o) {
+                constexpr int n = sizeof(o) / sizeof(o[0]);
+                if (!*(volatile int *)&ctl->any_bad)
+                    return;
+#pragma unroll 1
+                for (int jj = 0; jj < dl; ++jj) {
+                    if (!((ctl->bad[jj >> 5] >> (jj & 31)) & 1u) || !tree_sees(a, s, row_tok, jj))
+                        continue;
+                    const int64_t p = row0 + cl + jj;
+                    if constexpr (C::k8) {
+                        const float x = a.vs[p * 4 + d / 32] == 255 ? __uint_as_float(0x7fffffffu) : 0.f;
+#pragma unroll
+                        for (int e = 0; e < n; ++e)
+                            o[e] += x;
+                    } else {
+                        const uint2 *vr = reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.v) +
+                                                                          p * kTreeHD + d);
+#pragma unroll
+                        for (int e = 0; e < n; e += 4) {
+                            const uint2 w = vr[e / 4];
+                            const float y[4] = {bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y)};
+#pragma unroll
+                            for (int f = 0; f < 4; ++f)
+                                o[e + f] += fabsf(y[f]) <= 3.4e38f ? 0.f : y[f];
+                        }
+                    }
+                }
+            };
+            if constexpr (R > 1) {
+                // add the copies, through the ring, which is at rest
+                float *so = reinterpret_cast<float *>(ops);
+                float2 *sml = reinterpret_cast<float2 *>(so + 128 * kOPitch);   // maximum and sum
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    float o[32];
+                    umma::tmem_ld32(to + 32 * i, o);
+                    tmem_ld_wait_for(o);
+#pragma unroll
+                    for (int g = 0; g < 8; ++g)
+                        *reinterpret_cast<float4 *>(so + tid * kOPitch + 32 * i + 4 * g) =
+                            make_float4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
+                }
+                sml[tid] = make_float2(mref, l);
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                for (int x = warp; x < nrows; x += 4) {
+                    float M = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < R; ++w)
+                        M = fmaxf(M, sml[w * rt + x].x);
+                    float L = 0.f;
+                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int w = 0; w < R; ++w) {
+                        const float2 ml = sml[w * rt + x];
+                        const float f = ml.x > -INFINITY ? exp2f(ml.x - M) : (ml.y == 0.f ? 0.f : 1.f);
+                        const float4 y = *reinterpret_cast<const float4 *>(so + (w * rt + x) * kOPitch + lane * 4);
+                        L += f * ml.y;
+                        acc[0] = fmaf(f, y.x, acc[0]);
+                        acc[1] = fmaf(f, C::k8 ? y.z : y.y, acc[1]);
+                        acc[2] = fmaf(f, C::k8 ? y.y : y.z, acc[2]);
+                        acc[3] = fmaf(f, y.w, acc[3]);
+                    }
+                    const int xt = ctl->tok[x];
+                    add_bad(xt, lane * 4, acc);
+                    const int64_t at = ((int64_t)s * a.draft + xt) * a.n_q + j * a.rep + (run * rt + x) % a.rep;
+                    if (whole) {
+                        const float inv = L == 0.f ? 0.f : 1.f / L;
+                        reinterpret_cast<uint2 *>(a.out + at * kTreeHD)[lane] =
+                            make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv),
+                                       pack_bf16(acc[2] * inv, acc[3] * inv));
+                    } else {
+                        reinterpret_cast<float4 *>(a.part_o + ((int64_t)slot * rt + x) * kTreeHD)[lane] =
+                            make_float4(acc[0], acc[1], acc[2], acc[3]);
+                        if (lane == 0) {
+                            a.part_ml[(int64_t)slot * rt + x] = make_float2(M, L);
+                            if (blk0 == 0)
+                                a.join_rows[(int64_t)me * rt + x] = (int32_t)at;
+                        }
+                    }
+                }
+                fence_proxy_async_smem();          // the ring is written by copies next
+            } else {
+                const bool live = r < nrows;
+                const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                const int64_t at = ((int64_t)s * a.draft + max(tok, 0)) * a.n_q + j * a.rep + (run * rt + r) % a.rep;
+                if (any)
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        float o[32];
+                        umma::tmem_ld32(to + 32 * i, o);
+                        tmem_ld_wait_for(o);
+                        if (!live)
+                            continue;
+                        if (C::k8)                     // dims back in order
+#pragma unroll
+                            for (int e = 1; e < 32; e += 4) {
+                                const float x = o[e];
+                                o[e] = o[e + 1];
+                                o[e + 1] = x;
+                            }
+                        add_bad(tok, 32 * i, o);
+                        if (whole) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * kTreeHD + i * 32);
+#pragma unroll
+                            for (int g = 0; g < 4; ++g)
+                                dst[g] = make_uint4(pack_bf16(o[8 * g] * inv, o[8 * g + 1] * inv),
+                                                    pack_bf16(o[8 * g + 2] * inv, o[8 * g + 3] * inv),
+                                                    pack_bf16(o[8 * g + 4] * inv, o[8 * g + 5] * inv),
+                                                    pack_bf16(o[8 * g + 6] * inv, o[8 * g + 7] * inv));
+                        } else {
+                            float4 *dst = reinterpret_cast<float4 *>(
+                                a.part_o + ((int64_t)slot * rt + r) * kTreeHD + i * 32);
+#pragma unroll
+                            for (int g = 0; g < 8; ++g)
+                                dst[g] = make_float4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
+                        }
+                    }
+                if (live && !whole) {
+                    a.part_ml[(int64_t)slot * rt + r] = make_float2(mref, l);
+                    if (blk0 == 0)
+                        a.join_rows[(int64_t)me * rt + r] = (int32_t)at;
+                }
+            }
+        }
+        umma::fence_before_sync();
+    };
+
+    if (warp >= kMmaWarp) {
+        fewer_registers<C::kIssueRegs>();
+        if (warp == kMmaWarp) {
+            each_run(mma_role);
+            umma::fence_after_sync();
+            umma::tmem_dealloc(tmem, 512);
+        } else if (warp == kCopyWarp) {
+            each_run(copy_role);
+        } else if (warp == kPlanWarp) {
+            plan_role();
+        } else {
+            each_run([] {});
+        }
+    } else if (warp >= C::kSoftWarps) {
+        fewer_registers<C::kConvRegs>();
+        each_run(convert_role);
+    } else {
+        more_registers<C::kSoftRegs>();
+        if (R > 1) {                                  // the weights of other copies' keys: zero for good
+            const uint32_t zero[16] = {};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                tmem_st16(t_p + ((uint32_t)(warp & 3) << 21) + 16 * i, zero);
+            umma::tmem_st_wait();
+        }
+        each_run(softmax_role);
+    }
+    // zeros of the pairs that are skipped: last, when the CTAs wait for the slowest
+    tree_zero_skipped<kThreads>(a);
+    grid_launch_dependents();
+}
+
+template <int KIND, int NM, int R>
+int tiles_launch(const TreeArgs &a, int n, cudaStream_t s)
+{
+    using C = Cfg<KIND, NM>;
+    constexpr int rt = NM == 2 ? 256 : 128 / R;
+    constexpr size_t smem = C::kOffCtl + sizeof(TcCtl<C::kOps, C::kRaw, rt>);
+    auto kernel = attn_tree_tiles<KIND, NM, R>;
+    CUtensorMap map_k = {}, map_v = {};
+    // boxes of 128 rows x 128 bytes: half a bf16 row, or a row of codes (as 64 pairs)
+    const uint64_t rows = (uint64_t)a.n_seq * a.n_kv * (uint64_t)a.cap;
+    constexpr uint32_t cols = KIND == WIDE_KV_BF16 ? kTreeHD : kTreeHD / 2;
+    if (!make_tmap_2d_swz(&map_k, a.k, rows, cols, cols, kBK, 64, 128) ||
+        !make_tmap_2d_swz(&map_v, a.v, rows, cols, cols, kBK, 64, 128))
+        return WIDE_EUNSUPPORTED;
+    if (!raise_smem_limit(reinterpret_cast<const void *>(kernel), smem))
+        return WIDE_CUDA_FAIL();
+    // the roles' registers come out of what the block is launched with
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess)
+        return WIDE_CUDA_FAIL();
+    if (attr.numRegs != C::kLaunchRegs)
+        return WIDE_EUNSUPPORTED;
+    LaunchScope scope(KID_ATTN_TREE_TC, s);
+    kernel<<<n, C::kThreads, smem, s>>>(a, map_k, map_v);
+    return launch_status();
+}
+
+template <int KIND> int tiles_launch_rows(const TreeArgs &a, int rt, int n, cudaStream_t s)
+{
+    return rt == 32    ? tiles_launch<KIND, 1, 4>(a, n, s)
+           : rt == 64  ? tiles_launch<KIND, 1, 2>(a, n, s)
+           : rt == 128 ? tiles_launch<KIND, 1, 1>(a, n, s)
+                       : tiles_launch<KIND, 2, 1>(a, n, s);
+}
+
+}  // namespace
+
+int attn_tree_tiles_launch(const TreeArgs &a, int kind, int rt, int n, cudaStream_t s)
+{
+    return kind == WIDE_KV_BF16   ? tiles_launch_rows<WIDE_KV_BF16>(a, rt, n, s)
+           : kind == WIDE_KV_E4M3 ? tiles_launch_rows<WIDE_KV_E4M3>(a, rt, n, s)
+                                  : tiles_launch_rows<WIDE_KV_I8>(a, rt, n, s);
+}
+
+}  // namespace wide

@@ -122,6 +122,7 @@ enum KernelId : int32_t {
     KID_KV_READ = 23,
     KID_ATTN_TREE = 24,
     KID_ATTN_TREE_JOIN = 25,
+    KID_ATTN_TREE_TC = 26,
 };
 
 // Pointers of one masked-layer call (FFN pointers unused when !ffn).

@@ -87,4 +87,64 @@ __device__ __forceinline__ void kv_decode4(uint32_t w, float scale, float (&f)[4
     }
 }
 
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Multiplier that turns a code, moved into bf16 bits, into its value.  e4m3:
+// the bits stand for value * 2^-120, so the multiplier is 2^(b - 127 + 120);
+// above 2^127 (b > 134) the rest goes into a second one, kv_mult_high.
+template <int KIND> __device__ __forceinline__ uint32_t kv_mult(uint32_t b)
+{
+    if (b == 255u)
+        return 0x7fffu;
+    return (KIND == WIDE_KV_E4M3 ? min(b + 120u, 254u) : b) << 7;
+}
+__device__ __forceinline__ uint32_t kv_mult_high(uint32_t b)
+{
+    return (b > 134u && b < 255u ? b - 7u : 127u) << 7;
+}
+
+// Two codes, in the bytes of t that the kind wants (e4m3: the high byte of
+// each half; i8: the low byte; the other byte is ignored), as bf16 times mult.
+template <int KIND> __device__ __forceinline__ uint32_t kv_pair(uint32_t t, uint32_t mult)
+{
+    if constexpr (KIND == WIDE_KV_E4M3) {
+        // sign, exponent and mantissa to bf16's places: s eeee mmm -> s 0000eeee mmm0000
+        return mul_bf16x2(((t >> 4) & 0x07f007f0u) | (t & 0x80008000u), mult);
+    } else {
+        // 128 + (x & 127) as bf16, minus 128, or minus 256 if the sign bit is set
+        // (the common constant in a register: and-or with two immediates would
+        // be two instructions)
+        uint32_t c;
+        asm("mov.u32 %0, 0x43004300;" : "=r"(c));
+        const uint32_t u = (t & 0x007f007fu) | c, z = (t & 0x00800080u) | c;
+        return mul_bf16x2(sub_bf16x2(u, z), mult);
+    }
+}
+
+// The four codes of word x as bf16 times mult: bytes 0 and 2 in a, 1 and 3 in
+// b.  Bytes two apart are in the two halves already, so there is no permute:
+// five integer instructions for i8, seven for e4m3.
+template <int KIND>
+__device__ __forceinline__ void kv_pairs_0213(uint32_t x, uint32_t mult, uint32_t &a, uint32_t &b)
+{
+    if constexpr (KIND == WIDE_KV_E4M3) {
+        a = mul_bf16x2(((x << 4) & 0x07f007f0u) | ((x << 8) & 0x80008000u), mult);
+        b = mul_bf16x2(((x >> 4) & 0x07f007f0u) | (x & 0x80008000u), mult);
+    } else {
+        a = kv_pair<KIND>(x, mult);
+        b = kv_pair<KIND>(x >> 8, mult);
+    }
+}
+
 }  // namespace wide

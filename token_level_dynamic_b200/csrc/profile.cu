@@ -141,6 +141,8 @@ const char *wide_kernel_name(int32_t id)
         return "attn_tree";
     case KID_ATTN_TREE_JOIN:
         return "attn_tree_join";
+    case KID_ATTN_TREE_TC:
+        return "attn_tree_tiles";
     default:
         return "?";
     }
