@@ -566,7 +566,7 @@ constexpr int kCtasPerSm = 2;          // of attn_tree_rows
 // and CTAs.  Up to 16 rows attn_tree_rows, which needs no shared memory for the
 // keys (one token over 2048 keys 20 us and 29 ragged sequences in int8 104 us,
 // against 20 and 106 of attn_tree_tiles); above, its 16 rows a pass read and
-// convert the cache again (16 tokens over 131072 keys in e4m3: 354 us against 115).
+// convert the cache again (16 tokens over 131072 keys in e4m3: 354 us against 106).
 struct TreeChoice {
     int rt, n;
 };

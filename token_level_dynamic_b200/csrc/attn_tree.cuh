@@ -107,19 +107,23 @@ __device__ void tree_plan(const TreeArgs &a, int rt, int bk, int rc, uint32_t *c
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int U = a.n_seq * a.n_kv;
+#pragma unroll 1
     for (int s = warp; s < a.n_seq; s += THREADS / 32) {
         const int2 len = tree_lens(a, s, blockIdx.x == 0 && lane == 0);
         const int nb = (len.x + len.y + bk - 1) / bk;
+#pragma unroll 1
         for (int w = 0; w < (a.n_kv + 31) / 32; ++w) {
             const int nj = min(32, a.n_kv - 32 * w);
             int mine = 0;              // lane j: tokens that keep group 32 w + j
             if (!a.heads) {
                 mine = len.y;
             } else {
+#pragma unroll 1
                 for (int t0 = 0; t0 < len.y; t0 += 32) {
                     const int t = t0 + lane;
                     const uint32_t bits =
                         t < len.y ? a.heads[((size_t)s * a.draft + t) * a.Wh + w] : 0u;
+#pragma unroll 1
                     for (int j = 0; j < nj; ++j) {
                         const int c = __popc(__ballot_sync(0xffffffffu, (bits >> j) & 1u));
                         mine += lane == j ? c : 0;
@@ -140,6 +144,7 @@ __device__ void tree_plan(const TreeArgs &a, int rt, int bk, int rc, uint32_t *c
     const int per = (U + THREADS - 1) / THREADS;
     const int lo = min(U, tid * per), hi = min(U, lo + per);
     uint32_t sum = 0;
+#pragma unroll 1
     for (int i = lo; i < hi; ++i)
         sum += cum[i + 1];
     uint32_t inc = sum;
@@ -153,8 +158,10 @@ __device__ void tree_plan(const TreeArgs &a, int rt, int bk, int rc, uint32_t *c
         part[warp] = inc;
     __syncthreads();
     uint32_t before = inc - sum;
+#pragma unroll 1
     for (int w = 0; w < warp; ++w)
         before += part[w];
+#pragma unroll 1
     for (int i = lo; i < hi; ++i) {
         before += cum[i + 1];
         cum[i + 1] = before;
@@ -190,6 +197,7 @@ __device__ __forceinline__ void tree_tokens(const TreeArgs &a, int s, int j, int
 {
     const int lane = threadIdx.x & 31;
     int seen = 0;
+#pragma unroll 1
     for (int t0 = 0; t0 < dl && seen < to; t0 += 32) {
         const int t = t0 + lane;
         const bool on =
@@ -221,6 +229,7 @@ template <int THREADS> __device__ void tree_zero_skipped(const TreeArgs &a)
     const int lane = threadIdx.x & 31;
     const int64_t pairs = (int64_t)a.n_seq * a.draft * a.n_kv;
     const int64_t warps = (int64_t)gridDim.x * (THREADS / 32);
+#pragma unroll 1
     for (int64_t p0 = ((int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5)) * 32; p0 < pairs;
          p0 += warps * 32) {
         const int64_t p = p0 + lane;
@@ -238,6 +247,7 @@ template <int THREADS> __device__ void tree_zero_skipped(const TreeArgs &a)
             const int64_t t = z / a.n_kv;
             const int j = (int)(z - t * a.n_kv);
             uint4 *o = reinterpret_cast<uint4 *>(a.out + (t * a.n_q + (int64_t)j * a.rep) * kTreeHD);
+#pragma unroll 1
             for (int i = lane; i < a.rep * (kTreeHD / 8); i += 32)
                 o[i] = make_uint4(0u, 0u, 0u, 0u);
         }

@@ -1,39 +1,39 @@
 // attn_tree_tc.cu -- wide_attn_tree on the tensor cores: the rows of a run, up
 // to 256, share one pass over their keys.
 //
-// One persistent CTA per SM, 14 warps that hand work over through mbarriers:
-//   copy     one warp: tiles of 128 keys, then of their values, in turn, by
-//            TMA; bf16 straight into the operands' swizzled layout, 8-bit rows
-//            and their scales into a ring of raw tiles
-//   convert  8 warps (4 with two row halves): raw tiles to bf16 operand tiles,
-//            exactly, in a second ring.  A thread takes 32 codes with one
-//            scale; the bf16 pairs are bytes (0, 2) and (1, 3) of a word,
-//            which saves the permutes (integer instructions issue at half
-//            rate and are what bounds the conversion): the dims of an operand
-//            row are in the order 0 2 1 3 within each four, the queries are
-//            written in the same order and outputs put back at the end.  Values of new positions are checked:
-//            what is not finite is left out of the tile (0 * NaN would reach
-//            rows that do not attend it) and added to the attending rows at
-//            the end
+// One persistent CTA per SM, whose warps hand work over through mbarriers:
+//   copy     one warp: tiles of 128 keys and of 128 values, in the order in
+//            which the MMAs use them, by TMA; bf16 straight into the operands'
+//            swizzled layout, 8-bit rows and their scales into a ring of raw
+//            tiles
+//   convert  8 warps (4 for bf16): raw tiles to bf16 operand tiles, exactly, in
+//            a second ring.  A thread takes 32 codes with one scale; the bf16
+//            pairs are bytes (0, 2) and (1, 3) of a word, which saves the
+//            permutes (integer instructions issue at half rate): the dims of an
+//            operand row are in the order 0 2 1 3 within each four, the
+//            queries are written in the same order and outputs put back at the
+//            end.  Values of new positions are checked: what is not finite is
+//            left out of the tile (0 * NaN would reach rows that do not attend
+//            it) and added to the attending rows at the end
 //   MMA      one thread:  S = Q K^T  (M 128 rows, N 128 keys)  and
 //            O += P V  (N 128 dims), fp32 in tensor memory; P, rounded to
 //            bf16, is read from tensor memory too
-//   softmax  4 warps per 128 rows.  A row's reference maximum moves only when
-//            it grows by more than 8 (log2 units), to a whole number, so weights
-//            stay within 2^8 and O is rarely rescaled; a tile's weights are computed with the
-//            reference so far and once more in the rare case that it moves.
-// Row layouts of a run (R copies of rt = 128 / R rows, or two halves):
-//   R = 1    a thread per row takes all 128 keys of a tile
-//   R = 2, 4 the rows are repeated R times along M and a thread takes 128 / R
-//            keys of the tile: the copies' weights for other keys are zero.  A
-//            softmax warp's exponentials are the longest step with few rows
-//            (16 keys a clock and SM, but 4 for one warp), and this spreads
-//            them over the SM's quarters.  The copies are added at the end.
-//   NM = 2   256 rows: two tiles of scores and outputs, whose softmax and
-//            MMAs overlap each other.
-// Tensor memory, 512 columns: scores 0-127 and 128-255 (two tiles in turn, or
-// one per half), outputs from 256 (and 384), weights from 384 and 448 (with
-// two halves: over the first columns of their scores).
+//   softmax  two streams of 4 warps.  A row's reference maximum moves only
+//            when it grows by more than 8 (log2 units), to a whole number, so
+//            weights stay within 2^8 and O is rarely rescaled; weights are
+//            computed with the reference so far, and once more if it moves
+//   plan     one warp: the next run and its tokens
+// The two streams have scores, weights and output of their own, so that the
+// MMAs of one run during the softmax of the other: rows 0-127 and 128-255 of a
+// run of more than 128 rows, else the even and the odd tiles of the same rows,
+// whose outputs are added at the end.
+// Rows along M: a run of at most 64 or 32 rows is repeated R = 2 or 4 times,
+// and a thread takes 128 / R keys of a tile (the weights of a copy for other
+// keys are zero).  The softmax of a thread per row is the longest step with
+// few rows (a warp's exponentials all issue in one quarter of the SM), and
+// this spreads it over the quarters.  The copies are added at the end too.
+// Tensor memory, 512 columns: scores of the streams at 0 and 128, with the
+// weights over their first half; outputs at 256 and 384.
 #include "attn_tree.cuh"
 #include "host.h"
 #include "kv.cuh"
@@ -50,23 +50,21 @@ constexpr uint32_t kRawScales = kBK * 4;
 constexpr int kRunCost = 3;                      // tiles' time that a run costs beside its tiles
 constexpr int kOPitch = kTreeHD + 4;             // floats; row pitch when copies are added
 
+// NM: row halves of a run (2: up to 256 rows)
 template <int KIND, int NM> struct Cfg {
     static constexpr bool k8 = KIND != WIDE_KV_BF16;
     // warps, and registers per thread: every four warps the same number, out of
     // kLaunchRegs each (setmaxnreg); the last of the issuing four idles
-    static constexpr int kSoftWarps = 4 * NM, kConvWarps = !k8 ? 4 : NM == 2 ? 8 : 16;
-    static constexpr int kMmaWarp = kSoftWarps + kConvWarps, kCopyWarp = kMmaWarp + 1;
+    static constexpr int kSoftWarps = 8, kConvWarps = k8 ? 8 : 4;
+    static constexpr int kMmaWarp = kSoftWarps + kConvWarps, kCopyWarp = kMmaWarp + 1, kPlanWarp = kMmaWarp + 2;
     static constexpr int kWarps = kMmaWarp + 4, kThreads = 32 * kWarps;
-    static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-    static constexpr int kConvRegs = k8 ? (NM == 2 ? 72 : 64) : 72;
-    static constexpr int kIssueRegs = k8 && NM == 1 ? 56 : 72;
-    static constexpr int kSoftRegs =
-        (kLaunchRegs * kWarps - kConvRegs * kConvWarps - kIssueRegs * 4) / kSoftWarps / 8 * 8 > 232
-            ? 232
-            : (kLaunchRegs * kWarps - kConvRegs * kConvWarps - kIssueRegs * 4) / kSoftWarps / 8 * 8;
-    static_assert(kSoftRegs >= kLaunchRegs && kConvRegs <= kLaunchRegs && kIssueRegs <= kLaunchRegs, "registers");
-    static constexpr int kOps = k8 ? 5 - NM : 7 - NM;      // operand tiles
-    static constexpr int kRaw = k8 ? 5 - NM : 1;           // raw tiles (bf16: unused)
+    static constexpr int kLaunchRegs = k8 ? 96 : 128;
+    static constexpr int kConvRegs = 72, kIssueRegs = 64, kSoftRegs = k8 ? 136 : 184;
+    static_assert(kLaunchRegs * kThreads <= 65536 && kSoftRegs * kSoftWarps + kConvRegs * kConvWarps +
+                                                             kIssueRegs * 4 <= kLaunchRegs * kWarps,
+                  "registers");
+    static constexpr int kOps = k8 ? 3 : 7 - NM;           // operand tiles
+    static constexpr int kRaw = k8 ? 7 - 2 * NM : 1;       // raw tiles (bf16: unused)
     static constexpr uint32_t kOffOps = NM * kTile, kOffRaw = kOffOps + kOps * kTile;
     static constexpr uint32_t kOffScales = kOffRaw + (k8 ? kRaw * kRawCodes : 0);
     static constexpr uint32_t kOffCtl = kOffScales + (k8 ? kRaw * kRawScales : 0);
@@ -87,19 +85,16 @@ template <int OPS, int RAW, int ROWS> struct __align__(16) TcCtl {
     uint64_t op_empty[OPS];                      // the MMAs have read it
     uint64_t raw_full[RAW], raw_empty[RAW];      // raw rows landed / converted
     uint64_t q_full;                             // the run's queries are written
-    uint64_t s_full[2];                          // scores: of a row half, or of even / odd tiles
-    // (a buffer each, as the scores: a softmax warp may be a tile ahead of another)
+    // of the two streams
+    uint64_t s_full[2];                          // the scores are complete
     uint64_t p_full[2];                          // the weights are written (4 warps)
-    uint64_t pv_done[2];                         // O += P V is complete
+    uint64_t o_full[2];                          // the run's output is complete
     uint64_t all_done;                           // error path: every MMA is complete
     Run run;                                     // the current one; nt 0: there are no more
     uint32_t tmem;
     int abort, any_bad;
-    uint32_t first;                              // the plan: this CTA's places and the first's unit
-    uint32_t end, total;
-    int u0;
-    uint32_t base;
-    int16_t tok[ROWS], list[ROWS];               // token of each row, -1: none; tokens of the next run
+    int32_t at[ROWS];                            // output row of each row, -1: none
+    int16_t tok[ROWS], list[ROWS];               // its token; tokens of the next run
     uint32_t bad[kTreeMaxDraft / 32];            // new positions with a value that is not finite
 };
 
@@ -158,11 +153,11 @@ __device__ __forceinline__ void tmem_ld32w(uint32_t taddr, uint32_t *w)
 }
 
 // Weights 2^(sc x - mref) of COLS scores x in tensor memory as bf16 pairs;
-// returns the largest sc x and the sum of the weights.  TAIL: see(i) has the
+// returns the largest sc x and the sum of the weights.  tail: see(i) has the
 // bits of the scores 32 i .. that the row attends.
-template <int COLS, bool TAIL, class See>
+template <int COLS, class See>
 __device__ __forceinline__ float2 tile_weights(uint32_t ts, float sc, float mref, uint32_t (&pw)[COLS / 2],
-                                               See &&see)
+                                               bool tail, See &&see)
 {
     const float mb = mref > -INFINITY ? -mref : 0.f;
     const float2 sc2 = make_float2(sc, sc), mb2 = make_float2(mb, mb);
@@ -173,7 +168,7 @@ __device__ __forceinline__ float2 tile_weights(uint32_t ts, float sc, float mref
         float v[32];
         umma::tmem_ld32(ts + 32 * i, v);
         tmem_ld_wait_for(v);
-        if (TAIL) {
+        if (tail) {
             const uint32_t bits = see(i);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -202,6 +197,11 @@ template <int N> struct Ring {
             slot -= N;
             phase ^= 1u;
         }
+    }
+    __device__ __forceinline__ void back()
+    {
+        phase ^= slot == 0 ? 1u : 0u;
+        slot = slot == 0 ? N - 1 : slot - 1;
     }
 };
 
@@ -235,6 +235,18 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
         ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// Barrier of the 8 softmax warps; true if any thread says so.
+__device__ __forceinline__ bool softmax_barrier_or(bool say)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                 "barrier.cta.red.or.pred p, 1, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)say)
+                 : "memory");
+    return r != 0;
 }
 
 // True in one thread of a whole warp.
@@ -358,13 +370,12 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                     const __grid_constant__ CUtensorMap map_v)
 {
     using C = Cfg<KIND, NM>;
-    constexpr int kThreads = C::kThreads, kWarps = C::kWarps, kMmaWarp = C::kMmaWarp, kCopyWarp = C::kCopyWarp,
-                  kPlanWarp = C::kMmaWarp + 2;
+    constexpr int kThreads = C::kThreads, kMmaWarp = C::kMmaWarp, kCopyWarp = C::kCopyWarp, kPlanWarp = C::kPlanWarp;
     constexpr int rt = NM == 2 ? 256 : 128 / R;       // rows of a run
     constexpr int kCols = 128 / R;                    // keys of a tile per softmax thread
     using Ctl = TcCtl<C::kOps, C::kRaw, rt>;
     static_assert(C::kOffCtl + sizeof(Ctl) <= 227 * 1024, "shared memory");
-    static_assert(128 * (kOPitch * 4 + 8) <= C::kOps * kTile, "the copies' outputs fit in the ring");
+    static_assert(128 * (kOPitch * 4 + 8) <= C::kOps * kTile, "a stream's outputs fit in the ring");
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -380,46 +391,51 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
     uint8_t *ops = smem + C::kOffOps, *raw = smem + C::kOffRaw;
 
     // ---- the plan, in the ring of operand tiles
-    {
-        uint32_t *cum = reinterpret_cast<uint32_t *>(ops);
-        uint16_t *cnt = reinterpret_cast<uint16_t *>(cum + kTreeMaxUnits + 1);
-        uint32_t *part = reinterpret_cast<uint32_t *>(cnt + kTreeMaxUnits + 2);
-        static_assert((kTreeMaxUnits + 1) * 4 + (kTreeMaxUnits + 2) * 2 + kWarps * 4 <= C::kOps * kTile,
-                      "the plan fits in the ring");
-        tree_plan<kThreads>(a, rt, kBK, kRunCost, cum, cnt, part);
-        const uint32_t total = cum[U];
-        const int n_cta = tree_ctas((int)gridDim.x, total, rt);
-        if (me >= n_cta) {
-            if (tid == 0)
-                a.joins[me] = make_int4(0, 0, 0, 0);
-            tree_zero_skipped<kThreads>(a);
-            return;
+    uint32_t *cum = reinterpret_cast<uint32_t *>(ops);
+    uint16_t *cnt = reinterpret_cast<uint16_t *>(cum + kTreeMaxUnits + 1);
+    static_assert((kTreeMaxUnits + 1) * 4 + (kTreeMaxUnits + 2) * 2 + C::kWarps * 4 <= C::kOps * kTile,
+                  "the plan fits in the ring");
+    tree_plan<kThreads>(a, rt, kBK, kRunCost, cum, cnt, reinterpret_cast<uint32_t *>(cnt + kTreeMaxUnits + 2));
+    const uint32_t total = cum[U];
+    const int n_cta = tree_ctas((int)gridDim.x, total, rt);
+    if (me >= n_cta) {
+        if (tid == 0)
+            a.joins[me] = make_int4(0, 0, 0, 0);
+        if (warp < C::kSoftWarps)
+            tree_zero_skipped<32 * C::kSoftWarps>(a);
+        return;
+    }
+    const uint32_t first = (uint32_t)((uint64_t)me * total / n_cta);
+    const uint32_t end = (uint32_t)((uint64_t)(me + 1) * total / n_cta);
+    // of the plan warp: the 32 units from u0 on; lane i holds the places before
+    // unit u0 + i + 1, and the tokens of unit u0 + i
+    int u0 = 0, mine = 0;
+    uint32_t base = 0, upto = 0;
+    if (warp == kPlanWarp) {
+        u0 = tree_unit(cum, U, first);
+        base = cum[u0];
+        upto = cum[min(u0 + lane + 1, U)];
+        mine = u0 + lane < U ? cnt[u0 + lane] : 0;
+    }
+    if (tid == 0) {
+        ctl->abort = 0;
+        for (int i = 0; i < C::kOps; ++i) {
+            mbar_init(&ctl->op_full[i], 1);
+            mbar_init(&ctl->op_ready[i], C::kConvWarps);
+            mbar_init(&ctl->op_empty[i], 1);
         }
-        if (tid == 0) {
-            ctl->abort = 0;
-            ctl->total = total;
-            ctl->first = (uint32_t)((uint64_t)me * total / n_cta);
-            ctl->end = (uint32_t)((uint64_t)(me + 1) * total / n_cta);
-            ctl->u0 = tree_unit(cum, U, ctl->first);
-            ctl->base = cum[ctl->u0];
-            for (int i = 0; i < C::kOps; ++i) {
-                mbar_init(&ctl->op_full[i], 1);
-                mbar_init(&ctl->op_ready[i], C::kConvWarps);
-                mbar_init(&ctl->op_empty[i], 1);
-            }
-            for (int i = 0; i < C::kRaw; ++i) {
-                mbar_init(&ctl->raw_full[i], 33);
-                mbar_init(&ctl->raw_empty[i], C::kConvWarps);
-            }
-            mbar_init(&ctl->q_full, C::kConvWarps);
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(&ctl->s_full[i], 1);
-                mbar_init(&ctl->p_full[i], 4);
-                mbar_init(&ctl->pv_done[i], 1);
-            }
-            mbar_init(&ctl->all_done, 1);
-            fence_mbar_init();
+        for (int i = 0; i < C::kRaw; ++i) {
+            mbar_init(&ctl->raw_full[i], 33);
+            mbar_init(&ctl->raw_empty[i], C::kConvWarps);
         }
+        mbar_init(&ctl->q_full, C::kConvWarps);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->s_full[i], 1);
+            mbar_init(&ctl->p_full[i], 4);
+            mbar_init(&ctl->o_full[i], 1);
+        }
+        mbar_init(&ctl->all_done, 1);
+        fence_mbar_init();
     }
     if (warp == kMmaWarp) {
         umma::tmem_alloc(&ctl->tmem, 512);
@@ -434,18 +450,16 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
     __syncthreads();
     umma::fence_after_sync();
     const uint32_t tmem = ctl->tmem;
-    const uint32_t t_o = tmem + 256, t_p = NM == 2 ? tmem : tmem + 384;
-    constexpr uint32_t p_step = NM == 2 ? 128 : 64;   // columns from one weights buffer to the next
 
     // ring positions and parities that a role carries from run to run
     Ring<C::kRaw> raw_at;
     Ring<C::kOps> op_at;
-    uint32_t q_phase = 0;
-    // bit b: parity of the tiles that buffer b has held, and with it of the
-    // completions so far of s_full[b], p_full[b] and pv_done[b]
+    uint32_t runs = 0;                                // so far
+    // bit m: parity of the tiles of stream m so far, and with it of the
+    // completions of s_full[m] and p_full[m]
     uint32_t held = 0;
+    uint32_t o_phase = 0;                             // of this softmax warp's o_full
     bool ok = true;
-    const float sc = a.scale_log2;
     int *abort = &ctl->abort;
 
     // The runs of this CTA's places, one after another: each role calls it with
@@ -454,11 +468,12 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
     auto each_run = [&](auto &&work) {
         for (;;) {
             __syncthreads();
-            if (x.nt == 0)
+            const int nt = x.nt;
+            if (nt == 0)
                 break;
             work();
-            const int nt = x.nt;
             held ^= x.nm == 2 ? (nt & 1) * 3u : (((nt + 1) >> 1) & 1u) | ((nt >> 1) & 1u) << 1;
+            ++runs;
             if (__syncthreads_or(!ok))
                 break;
         }
@@ -468,20 +483,16 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
 
     // -------------------------------------------------------------- plan
     // One warp finds the next run and its tokens while the others work on the
-    // current one.  Lane i holds the places before unit u0 + i and after it,
-    // and its tokens.
+    // current one.
     auto plan_role = [&] {
-        const uint32_t total = ctl->total, end = ctl->end;
-        const int n_cta = tree_ctas((int)gridDim.x, total, rt);
-        int u0 = ctl->u0;
-        uint32_t b = ctl->first, base = ctl->base, upto = 0;
-        int mine = 0;
+        uint32_t b = first;
         int4 join = make_int4(0, 0, 0, 0);
         auto window = [&] {                           // of the 32 units from u0 on, `base` places before them
             const int u = u0 + lane, s = min(u, U - 1) / a.n_kv, j = u - s * a.n_kv;
             const int2 len = u < U ? tree_lens(a, s, false) : make_int2(0, 0);
             mine = a.heads ? 0 : len.y;
             if (a.heads)
+#pragma unroll 8
                 for (int t = 0; t < len.y; ++t)
                     mine += (a.heads[((size_t)s * a.draft + t) * a.Wh + (j >> 5)] >> (j & 31)) & 1u;
             upto = tree_places(mine * a.rep, rt, (len.x + len.y + kBK - 1) / kBK, kRunCost);
@@ -505,7 +516,7 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                     past = __ballot_sync(0xffffffffu, upto <= b);
                 }
                 const int i = __popc(past), u = u0 + i;    // upto rises with the lane
-                const uint32_t before = i ? __shfl_sync(0xffffffffu, upto, i - 1) : base;
+                const uint32_t prev = __shfl_sync(0xffffffffu, upto, max(i - 1, 0)), before = i ? prev : base;
                 r.s = u / a.n_kv;
                 r.j = u - r.s * a.n_kv;
                 const int2 len = tree_lens(a, r.s, false);
@@ -536,7 +547,6 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                 return true;
             }
         };
-        window();
         Run r;
         bool more = next(r);
         for (;;) {
@@ -547,8 +557,13 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
             ctl->bad[lane] = 0;
             if (more) {
                 const int lo = r.run * rt / a.rep;
-                for (int i = lane; i < rt; i += 32)
-                    ctl->tok[i] = i < r.nrows ? ctl->list[(r.run * rt + i) / a.rep - lo] : (int16_t)-1;
+#pragma unroll 1
+                for (int i = lane; i < rt; i += 32) {
+                    const int t = (r.run * rt + i) / a.rep, h = r.run * rt + i - t * a.rep;
+                    const int tok = i < r.nrows ? ctl->list[t - lo] : -1;
+                    ctl->tok[i] = (int16_t)tok;
+                    ctl->at[i] = tok < 0 ? -1 : (r.s * a.draft + tok) * a.n_q + r.j * a.rep + h;
+                }
             }
             __syncthreads();
             if (!more)
@@ -565,15 +580,25 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
         __syncthreads();
     };
 
+    // Operand tile i of a run, in the order of use: K of the first tile, then of
+    // each next tile before V of the one before it.  Returns the tile; values?
+    auto item = [](int i, int nt, bool &values) {
+        values = i > 0 && ((i & 1) == 0 || i == 2 * nt - 1);
+        return i == 0 ? 0 : i == 2 * nt - 1 ? nt - 1 : (i & 1) ? (i + 1) >> 1 : (i >> 1) - 1;
+    };
+
     // -------------------------------------------------------------- copy
     auto copy_role = [&] {
-        const int blk0 = x.blk0, nt = x.nt, cl = x.cl, dl = x.dl;
+        const int blk0 = x.blk0, nt = x.nt, nkeys = x.cl + x.dl;
         const int64_t row0 = x.row0;
-        const int nkeys = cl + dl;
-        if constexpr (C::k8) {
-            uint32_t issued = 0;
-            for (int i = 0; i < 2 * nt; ++i) {
-                const int p0 = (blk0 + (i >> 1)) * kBK;
+        uint32_t issued = 0;
+#pragma unroll 1
+        for (int i = 0; i < 2 * nt; ++i, ++issued) {
+            bool values;
+            const int p0 = (blk0 + item(i, nt, values)) * kBK;
+            const CUtensorMap *map = values ? &map_v : &map_k;
+            const int32_t y = (int32_t)(row0 + p0);
+            if constexpr (C::k8) {
                 ok = __all_sync(0xffffffffu, tc_wait(&ctl->raw_empty[raw_at.slot], raw_at.phase ^ 1u,
                                                      abort, a.status));
                 if (!ok)
@@ -582,10 +607,9 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                 if (lane == 0) {
                     // (rows past the unit's end may hold anything: finite with scale 0)
                     mbar_arrive_expect_tx(bar, kRawCodes);
-                    tma_load_2d(raw + raw_at.slot * kRawCodes, i & 1 ? &map_v : &map_k, 0,
-                                (int32_t)(row0 + p0), bar);
+                    tma_load_2d(raw + raw_at.slot * kRawCodes, map, 0, y, bar);
                 }
-                const uint8_t *scales = (i & 1 ? a.vs : a.ks) + (row0 + p0) * 4;
+                const uint8_t *scales = (values ? a.vs : a.ks) + (row0 + p0) * 4;
                 const uint32_t dst = smem_u32(smem + C::kOffScales + raw_at.slot * kRawScales);
 #pragma unroll
                 for (int r = lane; r < kBK; r += 32) {
@@ -594,66 +618,70 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                 }
                 cp_async_arrive_noinc(bar);
                 raw_at.next();
-                ++issued;
-            }
-            if (!ok) {                             // copies in flight land before shared memory goes
-                cp_async_wait_all();
-                Ring<C::kRaw> at = raw_at;
-                for (uint32_t i = 0; i < min(issued, (uint32_t)C::kRaw); ++i) {
-                    at.phase ^= at.slot == 0;
-                    at.slot = at.slot == 0 ? C::kRaw - 1 : at.slot - 1;
-                    mbar_wait(&ctl->raw_full[at.slot], at.phase);
-                }
-            }
-        } else if (lane == 0) {
-            uint32_t issued = 0;
-            for (int i = 0; i < 2 * nt; ++i) {
-                ok = tc_wait(&ctl->op_empty[op_at.slot], op_at.phase ^ 1u, abort, a.status);
+            } else {
+                ok = __all_sync(0xffffffffu, tc_wait(&ctl->op_empty[op_at.slot], op_at.phase ^ 1u, abort,
+                                                     a.status));
                 if (!ok)
                     break;
-                uint64_t *bar = &ctl->op_full[op_at.slot];
-                uint8_t *dst = ops + op_at.slot * kTile;
-                const int32_t y = (int32_t)(row0 + (int64_t)(blk0 + (i >> 1)) * kBK);
-                mbar_arrive_expect_tx(bar, kTile);
-                tma_load_2d(dst, i & 1 ? &map_v : &map_k, 0, y, bar);
-                tma_load_2d(dst + kHalf, i & 1 ? &map_v : &map_k, 64, y, bar);
+                if (lane == 0) {
+                    uint64_t *bar = &ctl->op_full[op_at.slot];
+                    uint8_t *dst = ops + op_at.slot * kTile;
+                    mbar_arrive_expect_tx(bar, kTile);
+                    tma_load_2d(dst, map, 0, y, bar);
+                    tma_load_2d(dst + kHalf, map, 64, y, bar);
+                }
                 op_at.next();
-                ++issued;
             }
-            if (!ok) {
-                Ring<C::kOps> at = op_at;
+        }
+        if (!ok) {                                    // copies in flight land before shared memory goes
+            if constexpr (C::k8) {
+                cp_async_wait_all();
+#pragma unroll 1
+                for (uint32_t i = 0; i < min(issued, (uint32_t)C::kRaw); ++i) {
+                    raw_at.back();
+                    mbar_wait(&ctl->raw_full[raw_at.slot], raw_at.phase);
+                }
+            } else {
+#pragma unroll 1
                 for (uint32_t i = 0; i < min(issued, (uint32_t)C::kOps); ++i) {
-                    at.phase ^= at.slot == 0;
-                    at.slot = at.slot == 0 ? C::kOps - 1 : at.slot - 1;
-                    mbar_wait(&ctl->op_full[at.slot], at.phase);
+                    op_at.back();
+                    mbar_wait(&ctl->op_full[op_at.slot], op_at.phase);
                 }
             }
         }
-        ok = __all_sync(0xffffffffu, ok);
     };
 
     // ----------------------------------------------------------- convert
     auto convert_role = [&] {
-        const int &s = x.s, &j = x.j, &run = x.run, &nm = x.nm;
         const int cl = x.cl, dl = x.dl, blk0 = x.blk0, nt = x.nt;
         constexpr int kConv = 32 * C::kConvWarps;
         const int ct = tid - 32 * C::kSoftWarps;
         // (8 bits) this thread's row of a tile, its swizzle pattern, and its first block of 32
         const int row = ct & 127, blk = ct >> 7;
         const uint32_t row_swz = swz128(row, 0);
-        // the queries first
-        for (int i = ct; i < nm * 128 * 16; i += kConv) {
-            const int r = i >> 4, c = i & 15, q_row = NM == 2 ? r : r % rt, tok = ctl->tok[q_row];
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (tok >= 0)
-                w = *reinterpret_cast<const uint4 *>(
-                    a.q + ((int64_t)s * a.draft + tok) * a.q_stride +
-                    (int64_t)(j * a.rep + (run * rt + q_row) % a.rep) * kTreeHD + c * 8);
-            if (C::k8)                                // dims in the operand order 0 2 1 3
-                w = make_uint4(__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632),
-                               __byte_perm(w.z, w.w, 0x5410), __byte_perm(w.z, w.w, 0x7632));
-            *reinterpret_cast<uint4 *>(smem + (r >> 7) * kTile + (c >> 3) * kHalf +
-                                       swz128(r & 127, c & 7)) = w;
+        // the queries first, 8 loads at a time
+#pragma unroll 1
+        for (int i0 = ct; i0 < x.nm * 128 * 16; i0 += 8 * kConv) {
+            uint4 w[8];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const int i = i0 + n * kConv, r = i >> 4, c = i & 15;
+                const int q_row = NM == 2 ? r : r & (rt - 1), at = ctl->at[q_row];
+                w[n] = make_uint4(0u, 0u, 0u, 0u);
+                if (at >= 0)
+                    w[n] = *reinterpret_cast<const uint4 *>(
+                        a.q + ((int64_t)x.s * a.draft + ctl->tok[q_row]) * a.q_stride +
+                        (int64_t)(at % a.n_q) * kTreeHD + c * 8);
+            }
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const int i = i0 + n * kConv, r = i >> 4, c = i & 15;
+                if (C::k8)                            // dims in the operand order 0 2 1 3
+                    w[n] = make_uint4(__byte_perm(w[n].x, w[n].y, 0x5410), __byte_perm(w[n].x, w[n].y, 0x7632),
+                                      __byte_perm(w[n].z, w[n].w, 0x5410), __byte_perm(w[n].z, w[n].w, 0x7632));
+                *reinterpret_cast<uint4 *>(smem + (r >> 7) * kTile + (c >> 3) * kHalf +
+                                           swz128(r & 127, c & 7)) = w[n];
+            }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -665,10 +693,11 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                 ctl->any_bad = 1;
             }
         };
+#pragma unroll 1
         for (int i = 0; i < 2 * nt && ok; ++i) {
-            const int p0 = (blk0 + (i >> 1)) * kBK;
-            const bool fresh = (i & 1) && p0 + kBK > cl;    // values with new positions
-            uint8_t *tile = ops + op_at.slot * kTile;
+            bool values;
+            const int p0 = (blk0 + item(i, nt, values)) * kBK;
+            const bool fresh = values && p0 + kBK > cl;         // values with new positions
             if constexpr (C::k8) {
                 constexpr int kN = kBK * 4 / kConv;             // blocks of 32 codes of a thread
                 ok = tc_wait(&ctl->raw_full[raw_at.slot], raw_at.phase, abort, a.status) &&
@@ -698,12 +727,15 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                 }
                 raw_at.next();
             } else {
-                ok = __all_sync(0xffffffffu, tc_wait(&ctl->op_full[op_at.slot], op_at.phase,
-                                                     abort, a.status));
-                if (ok && fresh) {
+                ok = __all_sync(0xffffffffu, tc_wait(&ctl->op_full[op_at.slot], op_at.phase, abort, a.status));
+                if (!ok)
+                    break;
+                if (fresh) {
                     // rows of new positions, and rows past the end, which may hold anything
-                    for (int x = max(cl - p0, 0) * 16 + ct; x < kBK * 16; x += kConv) {
-                        const int r = x >> 4, c = x & 15;
+                    uint8_t *tile = ops + op_at.slot * kTile;
+#pragma unroll 1
+                    for (int e = max(cl - p0, 0) * 16 + ct; e < kBK * 16; e += kConv) {
+                        const int r = e >> 4, c = e & 15;
                         uint4 *at = reinterpret_cast<uint4 *>(tile + (c >> 3) * kHalf + swz128(r, c & 7));
                         uint4 w = *at;
                         if (drop_not_finite(w)) {
@@ -714,7 +746,7 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
-                if (ok && lane == 0)
+                if (lane == 0)
                     mbar_arrive(&ctl->op_ready[op_at.slot]);
             }
             op_at.next();
@@ -729,98 +761,111 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
         const int nt = __shfl_sync(0xffffffffu, x.nt, 0);
         const bool two = NM == 2 && __shfl_sync(0xffffffffu, x.nm, 0) == 2;
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint32_t tm_p = NM == 2 ? tm : tm + 384;
         constexpr uint32_t idesc_s = umma::idesc_bf16_f32(128, 128);
         constexpr uint32_t idesc_pv = umma::idesc_bf16_f32_bmn(128, 128);
-        Ring<C::kOps> k_at = op_at, v_at = op_at;
-        v_at.next();
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             return __all_sync(0xffffffffu, tc_wait(bar, parity, abort, a.status));
         };
         auto ready = [&](const Ring<C::kOps> &at) {
             return (C::k8 || wait(&ctl->op_full[at.slot], at.phase)) && wait(&ctl->op_ready[at.slot], at.phase);
         };
-        // scores of tile t for row half m; the keys' slot is free after the last half
-        auto scores = [&](int t, int m, bool last) {
-            const uint32_t buf = two ? m : t & 1;
-            const uint64_t q0 = umma::desc_kmajor_sw128(smem_u32(smem) + (uint32_t)m * kTile);
-            const uint64_t k0 = umma::desc_kmajor_sw128(smem_u32(ops) + k_at.slot * kTile);
+        // S of stream m = rows m * half .. of Q times the tile at `at`; the last to read it frees it
+        auto scores = [&](const Ring<C::kOps> &at, int m, bool last) {
+            const uint64_t q0 = umma::desc_kmajor_sw128(smem_u32(smem) + (two ? (uint32_t)m * kTile : 0u));
+            const uint64_t k0 = umma::desc_kmajor_sw128(smem_u32(ops) + at.slot * kTile);
             umma::fence_after_sync();
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kTreeHD / 16; ++k) {
                     const uint32_t off = ((uint32_t)(k >> 2) * kHalf + (uint32_t)(k & 3) * 32u) >> 4;
-                    umma::mma_bf16(tm + buf * 128u, q0 + off, k0 + off, idesc_s, k != 0);
+                    umma::mma_bf16(tm + (uint32_t)m * 128u, q0 + off, k0 + off, idesc_s, k != 0);
                 }
-                umma::commit(&ctl->s_full[buf]);
+                umma::commit(&ctl->s_full[m]);
                 if (last)
-                    umma::commit(&ctl->op_empty[k_at.slot]);
+                    umma::commit(&ctl->op_empty[at.slot]);
             }
             __syncwarp();
-            if (last)
-                k_at.next(2);
         };
-        // O += P V of tile t for row half m
-        auto product = [&](int t, int m, bool last) {
-            const uint32_t buf = two ? m : t & 1;
-            const uint64_t v0 = umma::desc_mnmajor_sw128(smem_u32(ops) + v_at.slot * kTile, kHalf);
+        // O of stream m (+)= P V of the tile at `at`; end: the stream's last
+        auto product = [&](const Ring<C::kOps> &at, int m, bool add, bool last, bool end) {
+            const uint64_t v0 = umma::desc_mnmajor_sw128(smem_u32(ops) + at.slot * kTile, kHalf);
             umma::fence_after_sync();
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kBK / 16; ++k)
-                    mma_bf16_ta(tm + 256u + (uint32_t)m * 128u, tm_p + buf * p_step + (uint32_t)k * 8u,
-                                v0 + (uint32_t)k * (16u * 128u >> 4), idesc_pv, (t | k) != 0);
-                umma::commit(&ctl->pv_done[buf]);
+                    mma_bf16_ta(tm + 256u + (uint32_t)m * 128u, tm + (uint32_t)m * 128u + (uint32_t)k * 8u,
+                                v0 + (uint32_t)k * (16u * 128u >> 4), idesc_pv, add || k != 0);
+                if (end)
+                    umma::commit(&ctl->o_full[m]);
                 if (last)
-                    umma::commit(&ctl->op_empty[v_at.slot]);
+                    umma::commit(&ctl->op_empty[at.slot]);
             }
             __syncwarp();
-            if (last)
-                v_at.next(2);
         };
-        auto weights_ready = [&](int t, int m) {
-            const uint32_t buf = two ? m : t & 1;
-            return wait(&ctl->p_full[buf], ((held >> buf) + (uint32_t)(two ? t : t >> 1)) & 1u);
+        auto weights_ready = [&](int m, int i) {      // of the stream's tile i
+            return wait(&ctl->p_full[m], ((held >> m) + (uint32_t)i) & 1u);
         };
-        ok = wait(&ctl->q_full, q_phase) && ready(k_at);
+        // Scores of a stream's next tile come after the product that reads its
+        // weights, which lie over the scores: MMAs complete in order.
+        ok = wait(&ctl->q_full, runs & 1u) && ready(op_at);
         if (two) {
             if (ok) {
-                scores(0, 0, false);
-                scores(0, 1, true);
+                scores(op_at, 0, false);
+                scores(op_at, 1, true);
+                op_at.next();
             }
+#pragma unroll 1
             for (int t = 0; t < nt && ok; ++t) {
                 const bool more = t + 1 < nt;
-                ok = weights_ready(t, 0) && ready(v_at);
+                Ring<C::kOps> k_at = op_at, v_at = op_at;       // K of the next tile, V of this one
+                if (more)
+                    v_at.next();
+                ok = weights_ready(0, t) && ready(v_at);
                 if (!ok)
                     break;
-                product(t, 0, false);
-                if (more) {                           // after the product that reads the weights
+                product(v_at, 0, t > 0, false, !more);
+                if (more) {                                     // (complete before V is: the order of use)
                     ok = ready(k_at);
                     if (!ok)
                         break;
-                    scores(t + 1, 0, false);
+                    scores(k_at, 0, false);
                 }
-                ok = weights_ready(t, 1);
+                ok = weights_ready(1, t);
                 if (!ok)
                     break;
-                product(t, 1, true);
+                product(v_at, 1, t > 0, true, !more);
                 if (more)
-                    scores(t + 1, 1, true);
+                    scores(k_at, 1, true);
+                op_at = v_at;
+                op_at.next();
             }
         } else {
-            if (ok)
-                scores(0, 0, true);
-            for (int t = 0; t < nt && ok; ++t) {
-                if (t + 1 < nt) {
-                    ok = ready(k_at);
-                    if (!ok)
-                        break;
-                    scores(t + 1, 0, true);
+            // tile t is of stream t & 1:  S(0) S(1)  PV(0) S(2)  PV(1) S(3) ...
+            if (ok) {
+                scores(op_at, 0, true);
+                op_at.next();
+            }
+            if (ok && nt > 1) {
+                ok = ready(op_at);
+                if (ok) {
+                    scores(op_at, 1, true);
+                    op_at.next();
                 }
-                ok = weights_ready(t, 0) && ready(v_at);
+            }
+#pragma unroll 1
+            for (int t = 0; t < nt && ok; ++t) {
+                ok = weights_ready(t & 1, t >> 1) && ready(op_at);
                 if (!ok)
                     break;
-                product(t, 0, true);
+                product(op_at, t & 1, t > 1, true, t + 2 >= nt);
+                op_at.next();
+                if (t + 2 < nt) {
+                    ok = ready(op_at);
+                    if (!ok)
+                        break;
+                    scores(op_at, t & 1, true);
+                    op_at.next();
+                }
             }
         }
         if (!ok) {
@@ -830,42 +875,33 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
             __syncwarp();
             mbar_wait(&ctl->all_done, 0);
         }
-        op_at = k_at;
-        q_phase ^= 1u;
     };
 
     // ----------------------------------------------------------- softmax
     auto softmax_role = [&] {
         // (references: loaded from shared memory where they are used, not held in registers)
-        const int &s = x.s, &j = x.j, &dl = x.dl, &run = x.run, &nrows = x.nrows, &slot = x.slot, &whole = x.whole;
+        const int &s = x.s, &dl = x.dl, &nrows = x.nrows, &slot = x.slot, &whole = x.whole;
         const int64_t &row0 = x.row0;
-        const int cl = x.cl, blk0 = x.blk0, nt = x.nt;
-        if ((warp >> 2) >= x.nm)
-            return;
-        const int m = warp >> 2, quad = warp & 3;
-        const int r = NM == 2 ? tid : tid % rt;               // row of the run
-        const int c0 = NM == 2 ? 0 : tid / rt * kCols;        // first key of the tile
+        const int cl = x.cl, blk0 = x.blk0;
+        const bool two = NM == 2 && x.nm == 2;
+        const int m = warp >> 2, quad = warp & 3;             // stream; quarter of its lanes
+        const int r = two ? tid : NM == 2 ? tid & 127 : tid & (rt - 1);   // row of the run
+        const int c0 = R == 1 ? 0 : (tid & 127) / rt * kCols;  // first key of the tile
         const uint32_t lanes = (uint32_t)quad << 21;
-        const uint32_t to = t_o + (uint32_t)m * 128u + lanes;
+        const uint32_t ts = tmem + (uint32_t)m * 128u + lanes, to = ts + 256u;
         const int tok = ctl->tok[r];
-        const bool any = (NM == 2 ? warp * 32 : (quad * 32) % rt) < nrows;   // a live row in this warp
+        const bool any = (r & ~31) < nrows;                   // a live row in this warp
+        const int n = two ? x.nt : (x.nt + 1 - m) >> 1;       // the stream's tiles
+        const float sc = a.scale_log2;
         float mref = -INFINITY, l = 0.f;
-        const bool two = x.nm == 2;
-        for (int t = 0; t < nt; ++t) {
-            const int buf = two ? m : t & 1;
-            const uint32_t par = (held >> buf) + (uint32_t)(two ? t : t >> 1);
-            ok = tc_wait(&ctl->s_full[buf], par & 1u, abort, a.status);
-            // the buffer's last weights are read (complete already: the scores came after)
-            if (two ? t > 0 : t > 1)
-                ok = ok && tc_wait(&ctl->pv_done[buf], (par + 1u) & 1u, abort, a.status);
-            ok = __all_sync(0xffffffffu, ok);
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            ok = __all_sync(0xffffffffu, tc_wait(&ctl->s_full[m], ((held >> m) + (uint32_t)i) & 1u, abort, a.status));
             if (!ok)
                 break;
             umma::fence_after_sync();
             if (any) {
-                const uint32_t ts = tmem + (uint32_t)buf * 128u + lanes + (uint32_t)c0;
-                const int k0 = (blk0 + t) * kBK + c0;
-                const uint32_t tp = t_p + (uint32_t)buf * p_step + lanes + (uint32_t)(c0 / 2);
+                const int k0 = (blk0 + (two ? i : 2 * i + m)) * kBK + c0;
                 float alpha = 1.f;
                 // up to 64 keys at a time: their weights with the reference maximum so far, and
                 // once more if it moves
@@ -878,12 +914,8 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                     const int kh = k0 + h * kStep;
 #pragma unroll 1
                     for (int pass = 0;; ++pass) {
-                        if (kh + kStep > cl)
-                            w = tile_weights<kStep, true>(ts + h * kStep, sc, mref, pw, [&](int i) {
-                                return seen_bits(a, s, tok, kh + 32 * i, cl, dl);
-                            });
-                        else
-                            w = tile_weights<kStep, false>(ts + h * kStep, sc, mref, pw, [](int) { return 0u; });
+                        w = tile_weights<kStep>(ts + (uint32_t)(c0 + h * kStep), sc, mref, pw, kh + kStep > cl,
+                                                [&](int g) { return seen_bits(a, s, tok, kh + 32 * g, cl, dl); });
                         const bool up = w.x > mref + 8.f;
                         if (pass || !__any_sync(0xffffffffu, up))
                             break;
@@ -897,182 +929,224 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                     l = l * up_by + w.y;
                     alpha *= up_by;
                     if (h && __any_sync(0xffffffffu, up_by != 1.f)) {   // the weights stored before
-                        uint32_t y[kStep / 2];
-                        tmem_ld32w(tp, y);
+                        uint32_t y[32];
+                        umma::tmem_st_wait();
+                        tmem_ld32w(ts, y);
                         const uint32_t f = pack_bf16(up_by, up_by);
 #pragma unroll
-                        for (int e = 0; e < kStep / 2; ++e)
+                        for (int e = 0; e < 32; ++e)
                             y[e] = mul_bf16x2(y[e], f);
-#pragma unroll
-                        for (int i = 0; i < kStep / 32; ++i)
-                            tmem_st16(tp + 16 * i, y + 16 * i);
+                        tmem_st16(ts, y);
+                        tmem_st16(ts + 16, y + 16);
                     }
+                    if (R == 1) {
+                        // (over scores that this thread has read: 64 keys take 32 columns)
 #pragma unroll
-                    for (int i = 0; i < kStep / 32; ++i)
-                        tmem_st16(tp + h * (kStep / 2) + 16 * i, pw + 16 * i);
-                    umma::tmem_st_wait();
+                        for (int g = 0; g < kStep / 32; ++g)
+                            tmem_st16(ts + (uint32_t)(h * (kStep / 2) + 16 * g), pw + 16 * g);
+                    } else {
+                        const uint32_t zero[16] = {};
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {         // 32 keys of a tile each
+                            const int k = 32 * g - c0;
+                            if (k == 0)
+                                tmem_st16(ts + 16 * g, pw);
+                            else if (kStep > 32 && k == 32)
+                                tmem_st16(ts + 16 * g, pw + (kStep > 32 ? 16 : 0));
+                            else
+                                tmem_st16(ts + 16 * g, zero);
+                        }
+                    }
                 }
-                if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    if (!two) {                        // the product before must be complete
-                        ok = __all_sync(0xffffffffu, tc_wait(&ctl->pv_done[buf ^ 1],
-                                                             ((held >> (buf ^ 1)) + (uint32_t)((t - 1) >> 1)) & 1u,
-                                                             abort, a.status));
-                        if (!ok)
-                            break;
-                        umma::fence_after_sync();
-                    }
+                if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
-                    for (int i = 0; i < 4; ++i) {
+                    for (int g = 0; g < 4; ++g) {             // (the product before came before these scores)
                         float o[32];
-                        umma::tmem_ld32(to + 32 * i, o);
+                        umma::tmem_ld32(to + 32 * g, o);
                         tmem_ld_wait_for(o);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             o[e] *= alpha;
-                        umma::tmem_st32(to + 32 * i, o);
+                        umma::tmem_st32(to + 32 * g, o);
                     }
-                    umma::tmem_st_wait();
                 }
+                umma::tmem_st_wait();
             }
             umma::fence_before_sync();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&ctl->p_full[buf]);
+                mbar_arrive(&ctl->p_full[m]);
         }
-        if (ok) {
-            const int t = nt - 1, buf = two ? m : t & 1;
-            ok = __all_sync(0xffffffffu, tc_wait(&ctl->pv_done[buf],
-                                                 ((held >> buf) + (uint32_t)(two ? t : t >> 1)) & 1u,
-                                                 abort, a.status));
-        }
-        if (ok) {
-            umma::fence_after_sync();
-            // what is not finite in the new positions that the row of token row_tok attends, added
-            // to its elements d ..
-            auto add_bad = [&](int row_tok, int d, auto &o) {
-                constexpr int n = sizeof(o) / sizeof(o[0]);
-                if (!*(volatile int *)&ctl->any_bad)
-                    return;
+        if (ok && n > 0)
+            ok = __all_sync(0xffffffffu, tc_wait(&ctl->o_full[m], o_phase, abort, a.status));
+        o_phase ^= n > 0 ? 1u : 0u;
+        // both streams here or neither: they meet below
+        if (!two)
+            ok = !softmax_barrier_or(!ok);
+        if (!ok)
+            return;
+        umma::fence_after_sync();
+        // what is not finite in the new positions that the row of token row_tok attends, added
+        // to its elements d ..
+        auto add_bad = [&](int row_tok, int d, auto &o) {
+            constexpr int kE = sizeof(o) / sizeof(o[0]);
+            if (!*(volatile int *)&ctl->any_bad)
+                return;
 #pragma unroll 1
-                for (int jj = 0; jj < dl; ++jj) {
-                    if (!((ctl->bad[jj >> 5] >> (jj & 31)) & 1u) || !tree_sees(a, s, row_tok, jj))
-                        continue;
-                    const int64_t p = row0 + cl + jj;
-                    if constexpr (C::k8) {
-                        const float x = a.vs[p * 4 + d / 32] == 255 ? __uint_as_float(0x7fffffffu) : 0.f;
+            for (int jj = 0; jj < dl; ++jj) {
+                if (!((ctl->bad[jj >> 5] >> (jj & 31)) & 1u) || !tree_sees(a, s, row_tok, jj))
+                    continue;
+                const int64_t p = row0 + cl + jj;
+                if constexpr (C::k8) {
+                    const float y = a.vs[p * 4 + d / 32] == 255 ? __uint_as_float(0x7fffffffu) : 0.f;
 #pragma unroll
-                        for (int e = 0; e < n; ++e)
-                            o[e] += x;
-                    } else {
-                        const uint2 *vr = reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.v) +
-                                                                          p * kTreeHD + d);
+                    for (int e = 0; e < kE; ++e)
+                        o[e] += y;
+                } else {
+                    const uint2 *vr = reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.v) +
+                                                                      p * kTreeHD + d);
 #pragma unroll
-                        for (int e = 0; e < n; e += 4) {
-                            const uint2 w = vr[e / 4];
-                            const float y[4] = {bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y)};
+                    for (int e = 0; e < kE; e += 4) {
+                        const uint2 w = vr[e / 4];
+                        const float y[4] = {bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y)};
 #pragma unroll
-                            for (int f = 0; f < 4; ++f)
-                                o[e + f] += fabsf(y[f]) <= 3.4e38f ? 0.f : y[f];
-                        }
+                        for (int f = 0; f < 4; ++f)
+                            o[e + f] += fabsf(y[f]) <= 3.4e38f ? 0.f : y[f];
                     }
                 }
-            };
-            if constexpr (R > 1) {
-                // add the copies, through the ring, which is at rest
-                float *so = reinterpret_cast<float *>(ops);
-                float2 *sml = reinterpret_cast<float2 *>(so + 128 * kOPitch);   // maximum and sum
+            }
+        };
+        auto scale_of = [](float2 ml, float M) {              // of a part to the common maximum M
+            return ml.x > -INFINITY ? exp2f(ml.x - M) : (ml.y == 0.f ? 0.f : 1.f);
+        };
+        float *so = reinterpret_cast<float *>(ops);           // the ring, at rest: [128][kOPitch]
+        float2 *sml = reinterpret_cast<float2 *>(so + 128 * kOPitch);   // maximum and sum
+        float *mine_o = so + (tid & 127) * kOPitch;
+        float f0 = 1.f, f1 = 0.f;                             // scales of this stream's and the other's output
+        if (!two) {
+            if (m == 1) {
+                if (any && n > 0)
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    float o[32];
-                    umma::tmem_ld32(to + 32 * i, o);
-                    tmem_ld_wait_for(o);
-#pragma unroll
-                    for (int g = 0; g < 8; ++g)
-                        *reinterpret_cast<float4 *>(so + tid * kOPitch + 32 * i + 4 * g) =
-                            make_float4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
-                }
-                sml[tid] = make_float2(mref, l);
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                for (int x = warp; x < nrows; x += 4) {
-                    float M = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < R; ++w)
-                        M = fmaxf(M, sml[w * rt + x].x);
-                    float L = 0.f;
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int w = 0; w < R; ++w) {
-                        const float2 ml = sml[w * rt + x];
-                        const float f = ml.x > -INFINITY ? exp2f(ml.x - M) : (ml.y == 0.f ? 0.f : 1.f);
-                        const float4 y = *reinterpret_cast<const float4 *>(so + (w * rt + x) * kOPitch + lane * 4);
-                        L += f * ml.y;
-                        acc[0] = fmaf(f, y.x, acc[0]);
-                        acc[1] = fmaf(f, C::k8 ? y.z : y.y, acc[1]);
-                        acc[2] = fmaf(f, C::k8 ? y.y : y.z, acc[2]);
-                        acc[3] = fmaf(f, y.w, acc[3]);
-                    }
-                    const int xt = ctl->tok[x];
-                    add_bad(xt, lane * 4, acc);
-                    const int64_t at = ((int64_t)s * a.draft + xt) * a.n_q + j * a.rep + (run * rt + x) % a.rep;
-                    if (whole) {
-                        const float inv = L == 0.f ? 0.f : 1.f / L;
-                        reinterpret_cast<uint2 *>(a.out + at * kTreeHD)[lane] =
-                            make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv),
-                                       pack_bf16(acc[2] * inv, acc[3] * inv));
-                    } else {
-                        reinterpret_cast<float4 *>(a.part_o + ((int64_t)slot * rt + x) * kTreeHD)[lane] =
-                            make_float4(acc[0], acc[1], acc[2], acc[3]);
-                        if (lane == 0) {
-                            a.part_ml[(int64_t)slot * rt + x] = make_float2(M, L);
-                            if (blk0 == 0)
-                                a.join_rows[(int64_t)me * rt + x] = (int32_t)at;
-                        }
-                    }
-                }
-                fence_proxy_async_smem();          // the ring is written by copies next
-            } else {
-                const bool live = r < nrows;
-                const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-                const int64_t at = ((int64_t)s * a.draft + max(tok, 0)) * a.n_q + j * a.rep + (run * rt + r) % a.rep;
-                if (any)
-#pragma unroll 1
-                    for (int i = 0; i < 4; ++i) {
+                    for (int g = 0; g < 4; ++g) {
                         float o[32];
-                        umma::tmem_ld32(to + 32 * i, o);
+                        umma::tmem_ld32(to + 32 * g, o);
                         tmem_ld_wait_for(o);
-                        if (!live)
-                            continue;
-                        if (C::k8)                     // dims back in order
 #pragma unroll
-                            for (int e = 1; e < 32; e += 4) {
-                                const float x = o[e];
-                                o[e] = o[e + 1];
-                                o[e + 1] = x;
-                            }
-                        add_bad(tok, 32 * i, o);
-                        if (whole) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * kTreeHD + i * 32);
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(mine_o + 32 * g + e) =
+                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                sml[tid & 127] = make_float2(mref, l);
+            }
+            softmax_barrier_or(false);
+            if (m == 0) {
+                const float2 other = sml[tid];
+                const float M = fmaxf(mref, other.x);
+                f0 = scale_of(make_float2(mref, l), M);
+                f1 = scale_of(other, M);
+                l = f0 * l + f1 * other.y;
+                mref = M;
+            }
+        }
+        if (two || m == 0) {
+            const bool live = r < nrows;
+            const int64_t at = max(ctl->at[r], 0);
+            const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            if (any)
+#pragma unroll 1
+                for (int g = 0; g < 4; ++g) {
+                    float o[32];
+                    umma::tmem_ld32(to + 32 * g, o);
+                    tmem_ld_wait_for(o);
+                    if (!two && x.nt > 1) {                   // (else the other stream has no output)
 #pragma unroll
-                            for (int g = 0; g < 4; ++g)
-                                dst[g] = make_uint4(pack_bf16(o[8 * g] * inv, o[8 * g + 1] * inv),
-                                                    pack_bf16(o[8 * g + 2] * inv, o[8 * g + 3] * inv),
-                                                    pack_bf16(o[8 * g + 4] * inv, o[8 * g + 5] * inv),
-                                                    pack_bf16(o[8 * g + 6] * inv, o[8 * g + 7] * inv));
-                        } else {
-                            float4 *dst = reinterpret_cast<float4 *>(
-                                a.part_o + ((int64_t)slot * rt + r) * kTreeHD + i * 32);
-#pragma unroll
-                            for (int g = 0; g < 8; ++g)
-                                dst[g] = make_float4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 y = *reinterpret_cast<const float4 *>(mine_o + 32 * g + e);
+                            o[e] = fmaf(f1, y.x, f0 * o[e]);
+                            o[e + 1] = fmaf(f1, y.y, f0 * o[e + 1]);
+                            o[e + 2] = fmaf(f1, y.z, f0 * o[e + 2]);
+                            o[e + 3] = fmaf(f1, y.w, f0 * o[e + 3]);
                         }
                     }
-                if (live && !whole) {
-                    a.part_ml[(int64_t)slot * rt + r] = make_float2(mref, l);
-                    if (blk0 == 0)
-                        a.join_rows[(int64_t)me * rt + r] = (int32_t)at;
+                    if (C::k8)                                // dims back in order
+#pragma unroll
+                        for (int e = 1; e < 32; e += 4) {
+                            const float y = o[e];
+                            o[e] = o[e + 1];
+                            o[e + 1] = y;
+                        }
+                    if constexpr (R > 1) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(mine_o + 32 * g + e) =
+                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    } else if (live) {
+                        add_bad(tok, 32 * g, o);
+                        if (whole) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * kTreeHD + g * 32);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                                    pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                                    pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                                    pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                        } else {
+                            float4 *dst = reinterpret_cast<float4 *>(a.part_o + ((int64_t)slot * rt + r) * kTreeHD +
+                                                                     g * 32);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        }
+                    }
+                }
+            if constexpr (R > 1) {
+                sml[tid & 127] = make_float2(mref, l);
+            } else if (live && !whole) {
+                a.part_ml[(int64_t)slot * rt + r] = make_float2(mref, l);
+                if (blk0 == 0)
+                    a.join_rows[(int64_t)me * rt + r] = (int32_t)at;
+            }
+        }
+        if constexpr (R > 1) {                                // add the copies
+            softmax_barrier_or(false);
+#pragma unroll 1
+            for (int row = warp; row < nrows; row += 8) {
+                float M = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < R; ++c)
+                    M = fmaxf(M, sml[c * rt + row].x);
+                float L = 0.f;
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < R; ++c) {
+                    const float2 ml = sml[c * rt + row];
+                    const float f = scale_of(ml, M);
+                    const float4 y = *reinterpret_cast<const float4 *>(so + (c * rt + row) * kOPitch + lane * 4);
+                    L += f * ml.y;
+                    acc[0] = fmaf(f, y.x, acc[0]);
+                    acc[1] = fmaf(f, y.y, acc[1]);
+                    acc[2] = fmaf(f, y.z, acc[2]);
+                    acc[3] = fmaf(f, y.w, acc[3]);
+                }
+                add_bad(ctl->tok[row], lane * 4, acc);
+                const int64_t at = ctl->at[row];
+                if (whole) {
+                    const float inv = L == 0.f ? 0.f : 1.f / L;
+                    reinterpret_cast<uint2 *>(a.out + at * kTreeHD)[lane] =
+                        make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+                } else {
+                    reinterpret_cast<float4 *>(a.part_o + ((int64_t)slot * rt + row) * kTreeHD)[lane] =
+                        make_float4(acc[0], acc[1], acc[2], acc[3]);
+                    if (lane == 0) {
+                        a.part_ml[(int64_t)slot * rt + row] = make_float2(M, L);
+                        if (blk0 == 0)
+                            a.join_rows[(int64_t)me * rt + row] = (int32_t)at;
+                    }
                 }
             }
         }
+        if (!two)
+            fence_proxy_async_smem();                         // the ring is written by copies next
         umma::fence_before_sync();
     };
 
@@ -1094,17 +1168,10 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
         each_run(convert_role);
     } else {
         more_registers<C::kSoftRegs>();
-        if (R > 1) {                                  // the weights of other copies' keys: zero for good
-            const uint32_t zero[16] = {};
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                tmem_st16(t_p + ((uint32_t)(warp & 3) << 21) + 16 * i, zero);
-            umma::tmem_st_wait();
-        }
         each_run(softmax_role);
+        // zeros of the pairs that are skipped: last, when the CTAs wait for the slowest
+        tree_zero_skipped<32 * C::kSoftWarps>(a);
     }
-    // zeros of the pairs that are skipped: last, when the CTAs wait for the slowest
-    tree_zero_skipped<kThreads>(a);
     grid_launch_dependents();
 }
 
