@@ -14,6 +14,7 @@ skipping (2.C).
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -494,13 +495,46 @@ def wide_rope_config(rot_dim: int, theta: float = 5e5, layout: int = WIDE_ROPE_H
                           amplitude)
 
 
-def _index(t, name: str, n: int, device):
+# The serving operators below are called per layer and step, often on a few
+# rows, where the host's time for a call is all of it: they read each tensor
+# attribute once and enter a device or stream context only where it differs
+# from the current one.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _device_of(fn: str, **tensors) -> int:
+    """Index of the CUDA device every given tensor is on, as _one_device."""
+    dev = -1
+    for t in tensors.values():
+        if t is not None:
+            d = t.get_device()
+            if d < 0 or d != dev and dev >= 0:
+                _one_device(fn, **tensors)
+            dev = d
+    return dev
+
+
+def _invoke(fn: str, dev: int, stream, *args) -> None:
+    """The entry point on device dev and the given (None: dev's current) stream."""
+    stream = _raw_stream(dev) if stream is None else _stream(stream, dev)
+    if torch.cuda.current_device() == dev:
+        rc = getattr(_L, fn)(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(_L, fn)(*args, stream)
+    if rc != WIDE_OK:
+        raise WideError(fn, rc)
+
+
+def _index(t, name: str, n: int):
     """Device pointer of an int32 vector of n elements (None: NULL)."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n:
+    if t.dtype is not torch.int32 or t.shape != (n,):
         raise ValueError(f"{name} must be int32 [{n}], got {t.dtype} {tuple(t.shape)}")
-    return _dev_ptr(t, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def wide_rope(x: torch.Tensor, positions: torch.Tensor, rope: WideRopeConfig,
@@ -510,20 +544,18 @@ def wide_rope(x: torch.Tensor, positions: torch.Tensor, rope: WideRopeConfig,
     position (int32 [T]).  ``out`` may be x."""
     if x.dim() != 3:
         raise ValueError(f"x must be [T][heads][head_dim], got {tuple(x.shape)}")
-    T, n, hd = x.shape
+    T, n, hd = shape = x.shape
     if out is None:
-        out = torch.empty((T, n, hd), dtype=x.dtype, device=x.device)
-    elif out.dtype != x.dtype or out.shape != x.shape:
-        raise ValueError(f"out must be {x.dtype} {tuple(x.shape)}")
-    if (x.stride(2) != 1 and hd > 1) or (out.stride(2) != 1 and hd > 1):
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif out.dtype is not x.dtype or out.shape != shape:
+        raise ValueError(f"out must be {x.dtype} {tuple(shape)}")
+    xt, xh, xe = x.stride()
+    ot, oh, oe = out.stride()
+    if (xe != 1 or oe != 1) and hd > 1:
         raise ValueError("the elements of a head must be contiguous")
-    dev = _one_device("wide_rope", x=x, positions=positions, out=out)
-    d = WideRopeDims(T, n, hd, _dtype_code(x), x.stride(0), x.stride(1), out.stride(0),
-                     out.stride(1))
-    pos = _index(positions, "positions", T, dev)
-    with torch.cuda.device(dev):
-        _check("wide_rope", _L.wide_rope(x.data_ptr(), pos, out.data_ptr(), ctypes.byref(d),
-                                         ctypes.byref(rope), _stream(stream, dev)))
+    dev = _device_of("wide_rope", x=x, positions=positions, out=out)
+    _invoke("wide_rope", dev, stream, x.data_ptr(), _index(positions, "positions", T),
+            out.data_ptr(), WideRopeDims(T, n, hd, _dtype_code(x), xt, xh, ot, oh), rope)
     return out
 
 
@@ -550,38 +582,48 @@ def wide_kv_cache(n_seq: int, n_kv: int, cap: int, dtype=torch.bfloat16, head_di
     return cache
 
 
-def _cache_tensors(cache: dict) -> dict:
-    return {"cache_" + n: cache.get(n) for n in ("k", "v", "k_scale", "v_scale")}
-
-
-def _kv_cache(cache: dict) -> WideKVCache:
+def _kv_cache(cache: dict, dev: int = None) -> WideKVCache:
+    """The cache's description; its tensors must be on device dev (None: any one)."""
     k, v = cache["k"], cache["v"]
-    if k.dtype not in _KV_KINDS or v.dtype != k.dtype:
+    kind = _KV_KINDS.get(k.dtype)
+    if kind is None or v.dtype is not k.dtype:
         raise TypeError(f"unsupported cache dtypes {k.dtype}, {v.dtype}")
-    if k.dim() != 4 or v.shape != k.shape:
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape:
         raise ValueError(f"cache k and v must be [n_seq][n_kv][cap][head_dim], got "
-                         f"{tuple(k.shape)}, {tuple(v.shape)}")
-    n_seq, n_kv, cap, hd = k.shape
+                         f"{tuple(shape)}, {tuple(v.shape)}")
+    n_seq, n_kv, cap, hd = shape
+    d = k.get_device() if dev is None else dev
+    fine = d >= 0 and k.get_device() == d and v.get_device() == d and k.is_contiguous() and \
+        v.is_contiguous()
     ks = vs = None
-    if k.dtype != torch.bfloat16:
-        for n in ("k_scale", "v_scale"):
-            t = cache.get(n)
-            if t is None or t.dtype != torch.uint8 or \
-                    tuple(t.shape) != (n_seq, n_kv, cap, hd // 32):
+    if kind != WIDE_KV_BF16:
+        want = (n_seq, n_kv, cap, hd // 32)
+        ks, vs = cache.get("k_scale"), cache.get("v_scale")
+        for n, t in (("k_scale", ks), ("v_scale", vs)):
+            if t is None or t.dtype is not torch.uint8 or t.shape != want:
                 raise ValueError(f"cache {n} must be uint8 [{n_seq}][{n_kv}][{cap}][{hd // 32}]")
-        ks, vs = _dev_ptr(cache["k_scale"], "k_scale"), _dev_ptr(cache["v_scale"], "v_scale")
-    return WideKVCache(_dev_ptr(k, "k"), _dev_ptr(v, "v"), ks, vs, n_seq, cap, n_kv, hd,
-                       _KV_KINDS[k.dtype])
+            fine = fine and t.get_device() == d and t.is_contiguous()
+    if not fine:
+        for n, t in (("k", k), ("v", v), ("k_scale", ks), ("v_scale", vs)):
+            if t is not None:
+                _dev_ptr(t, f"cache {n}")
+        raise ValueError(f"cache is not on one device with the other operands (cuda:{d})")
+    return WideKVCache(k.data_ptr(), v.data_ptr(), ks if ks is None else ks.data_ptr(),
+                       vs if vs is None else vs.data_ptr(), n_seq, cap, n_kv, hd, kind)
 
 
 def _kv_rows(k, v, T: int, n_kv: int, hd: int, seq_len: int) -> WideKVRows:
+    want = (T, n_kv, hd)
     for name, t in (("k", k), ("v", v)):
-        if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, n_kv, hd):
+        if t.dtype is not torch.bfloat16 or t.shape != want:
             raise ValueError(f"{name} must be bfloat16 [{T}][{n_kv}][{hd}], got {t.dtype} "
                              f"{tuple(t.shape)}")
-        if t.stride(2) != 1:
-            raise ValueError(f"the elements of a head of {name} must be contiguous")
-    return WideKVRows(seq_len, k.stride(0), k.stride(1), v.stride(0), v.stride(1))
+    kt, kh, ke = k.stride()
+    vt, vh, ve = v.stride()
+    if ke != 1 or ve != 1:
+        raise ValueError("the elements of a head of k and v must be contiguous")
+    return WideKVRows(seq_len, kt, kh, vt, vh)
 
 
 def wide_kv_append(k: torch.Tensor, v: torch.Tensor, cache: dict, start: torch.Tensor = None,
@@ -596,15 +638,10 @@ def wide_kv_append(k: torch.Tensor, v: torch.Tensor, cache: dict, start: torch.T
     if n_seq == 0 or T % n_seq != 0:
         raise ValueError(f"{T} rows do not divide into {n_seq} sequences")
     rows = _kv_rows(k, v, T, n_kv, hd, T // n_seq)
-    dev = _one_device("wide_kv_append", k=k, v=v, start=start, count=count, positions=positions,
-                      **_cache_tensors(cache))
-    c = _kv_cache(cache)
-    st, ct = _index(start, "start", n_seq, dev), _index(count, "count", n_seq, dev)
-    ps = _index(positions, "positions", T, dev)
-    with torch.cuda.device(dev):
-        _check("wide_kv_append", _L.wide_kv_append(
-            k.data_ptr(), v.data_ptr(), ctypes.byref(c), st, ct, ps, ctypes.byref(rows),
-            None if rope is None else ctypes.byref(rope), _stream(stream, dev)))
+    dev = _device_of("wide_kv_append", k=k, v=v, start=start, count=count, positions=positions)
+    _invoke("wide_kv_append", dev, stream, k.data_ptr(), v.data_ptr(), _kv_cache(cache, dev),
+            _index(start, "start", n_seq), _index(count, "count", n_seq),
+            _index(positions, "positions", T), rows, rope)
 
 
 def wide_kv_read(cache: dict, start: torch.Tensor, seq_len: int, count: torch.Tensor = None,
@@ -620,23 +657,28 @@ def wide_kv_read(cache: dict, start: torch.Tensor, seq_len: int, count: torch.Te
     if v is None:
         v = make((T, n_kv, hd), dtype=torch.bfloat16, device=cache["k"].device)
     rows = _kv_rows(k, v, T, n_kv, hd, seq_len)
-    dev = _one_device("wide_kv_read", k=k, v=v, start=start, count=count,
-                      **_cache_tensors(cache))
-    c = _kv_cache(cache)
-    st, ct = _index(start, "start", n_seq, dev), _index(count, "count", n_seq, dev)
-    with torch.cuda.device(dev):
-        _check("wide_kv_read", _L.wide_kv_read(k.data_ptr(), v.data_ptr(), ctypes.byref(c), st, ct,
-                                               ctypes.byref(rows), _stream(stream, dev)))
+    dev = _device_of("wide_kv_read", k=k, v=v, start=start, count=count)
+    _invoke("wide_kv_read", dev, stream, k.data_ptr(), v.data_ptr(), _kv_cache(cache, dev),
+            _index(start, "start", n_seq), _index(count, "count", n_seq), rows)
     return k, v
 
 
 # ------------------------------------------------ attention of draft trees
 
+@functools.lru_cache(maxsize=256)
+def _attn_tree_workspace(dev: int, n_seq: int, n_kv: int, cap: int, hd: int, kind: int,
+                         draft: int, n_q: int) -> int:
+    # (a size: the pointers only have to pass the checks)
+    c = WideKVCache(256, 256, 256, 256, n_seq, cap, n_kv, hd, kind)
+    with torch.cuda.device(dev):
+        return int(_L.wide_attn_tree_workspace_bytes(
+            c, WideAttnTreeDims(draft, n_q * hd, n_q, 1.0)))
+
+
 def wide_attn_tree_workspace_bytes(cache: dict, draft: int, n_q: int) -> int:
     c = _kv_cache(cache)
-    d = WideAttnTreeDims(draft, n_q * c.head_dim, n_q, 1.0)
-    with torch.cuda.device(cache["k"].device):
-        return int(_L.wide_attn_tree_workspace_bytes(ctypes.byref(c), ctypes.byref(d)))
+    return _attn_tree_workspace(cache["k"].get_device(), c.n_seq, c.n_kv, c.cap, c.head_dim,
+                                c.kind, draft, n_q)
 
 
 def wide_attn_tree(q: torch.Tensor, cache: dict, cache_len: torch.Tensor,
@@ -650,38 +692,42 @@ def wide_attn_tree(q: torch.Tensor, cache: dict, cache_len: torch.Tensor,
     head_mask int32 words [T][ceil(n_kv / 32)] (None: all kept); scale None:
     1 / sqrt(128).  Returns out bf16 [T][n_q][128]; tokens past draft_len are
     left as they were (zeros when out is not given)."""
-    if q.dim() != 3 or q.dtype != torch.bfloat16:
-        raise ValueError(f"q must be bfloat16 [T][n_q][head_dim], got {q.dtype} {tuple(q.shape)}")
+    shape = q.shape
+    if len(shape) != 3 or q.dtype is not torch.bfloat16:
+        raise ValueError(f"q must be bfloat16 [T][n_q][head_dim], got {q.dtype} {tuple(shape)}")
+    T, n_q, hd = shape
+    qt, qh, qe = q.stride()
     c = _kv_cache(cache)
-    T, n_q, hd = q.shape
-    if c.n_seq == 0 or T % c.n_seq != 0 or T == 0:
-        raise ValueError(f"{T} tokens do not divide into {c.n_seq} sequences")
-    draft = T // c.n_seq
-    if hd != c.head_dim or q.stride(2) != 1 or (q.stride(1) != hd and n_q > 1):
+    dev = _device_of("wide_attn_tree", q=q, cache_len=cache_len, tree_mask=tree_mask,
+                     head_mask=head_mask, draft_len=draft_len, out=out, workspace=workspace,
+                     cache_k=cache["k"])
+    n_seq, n_kv = c.n_seq, c.n_kv
+    if n_seq == 0 or T % n_seq != 0 or T == 0:
+        raise ValueError(f"{T} tokens do not divide into {n_seq} sequences")
+    draft = T // n_seq
+    if hd != c.head_dim or qe != 1 or (qh != hd and n_q > 1):
         raise ValueError(f"the heads of a token of q must be contiguous rows of {c.head_dim}")
-    for name, m, n in (("tree_mask", tree_mask, draft), ("head_mask", head_mask, c.n_kv)):
-        if m is not None and (m.dtype != torch.int32 or tuple(m.shape) != (T, (n + 31) // 32)):
-            raise ValueError(f"{name} must be int32 [{T}][{(n + 31) // 32}], got {m.dtype} "
-                             f"{tuple(m.shape)}")
+    masks = [None, None]
+    for i, (name, m, n) in enumerate((("tree_mask", tree_mask, draft),
+                                      ("head_mask", head_mask, n_kv))):
+        if m is not None:
+            if m.dtype is not torch.int32 or m.shape != (T, (n + 31) // 32):
+                raise ValueError(f"{name} must be int32 [{T}][{(n + 31) // 32}], got {m.dtype} "
+                                 f"{tuple(m.shape)}")
+            masks[i] = _dev_ptr(m, name)
     if out is None:
         make = torch.empty if draft_len is None else torch.zeros
-        out = make((T, n_q, hd), dtype=torch.bfloat16, device=q.device)
-    elif out.dtype != torch.bfloat16 or out.shape != q.shape:
-        raise ValueError(f"out must be bfloat16 {tuple(q.shape)}")
-    dev = _one_device("wide_attn_tree", q=q, cache_len=cache_len, tree_mask=tree_mask,
-                      head_mask=head_mask, draft_len=draft_len, out=out, workspace=workspace,
-                      **_cache_tensors(cache))
-    cl, dl = _index(cache_len, "cache_len", c.n_seq, dev), _index(draft_len, "draft_len", c.n_seq, dev)
-    d = WideAttnTreeDims(draft, q.stride(0) if T > 1 else n_q * hd, n_q,
+        out = make(shape, dtype=torch.bfloat16, device=q.device)
+    elif out.dtype is not torch.bfloat16 or out.shape != shape:
+        raise ValueError(f"out must be bfloat16 {tuple(shape)}")
+    need = max(256, _attn_tree_workspace(dev, n_seq, n_kv, c.cap, hd, c.kind, draft, n_q))
+    if workspace is None or workspace.nbytes < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    d = WideAttnTreeDims(draft, qt if T > 1 else n_q * hd, n_q,
                          hd ** -0.5 if scale is None else scale)
-    with torch.cuda.device(dev):
-        need = int(_L.wide_attn_tree_workspace_bytes(ctypes.byref(c), ctypes.byref(d)))
-        if workspace is None or workspace.numel() < need:
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        _check("wide_attn_tree", _L.wide_attn_tree(
-            q.data_ptr(), ctypes.byref(c), cl, dl,
-            None if tree_mask is None else _dev_ptr(tree_mask, "tree_mask"),
-            None if head_mask is None else _dev_ptr(head_mask, "head_mask"),
-            _dev_ptr(out, "out"), ctypes.byref(d), workspace.data_ptr(), workspace.numel(),
-            _stream(stream, dev)))
+    _invoke("wide_attn_tree", dev, stream, q.data_ptr(), c, _index(cache_len, "cache_len", n_seq),
+            _index(draft_len, "draft_len", n_seq), masks[0], masks[1], _dev_ptr(out, "out"), d,
+            workspace.data_ptr(), workspace.nbytes)
     return out

@@ -26,22 +26,29 @@ bool rope_table(const wide_rope_config *c, RopeTable *t)
     const bool ramp = c->factor != 1.0 && c->original_len > 0;
     if (ramp && (!(c->low_freq >= 0.0) || !(c->high_freq > c->low_freq) || !isfinite(c->high_freq)))
         return false;
+    // theta^(-2 i / rot_dim) for i = 8 a + b as a product of two powers: 24
+    // calls of pow instead of 128, off by 3 units of 2^-53
     const double two_pi = 6.283185307179586476925286766559;
-    for (int i = 0; i < kRopeMaxPairs; ++i) {
-        double f = 0.0;
-        if (i < c->rot_dim / 2) {
-            f = pow(c->theta, -2.0 * i / c->rot_dim);
-            if (ramp) {
-                const double r = (double)c->original_len * f / two_pi;
-                double g = (r - c->low_freq) / (c->high_freq - c->low_freq);
-                g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
-                f *= g + (1.0 - g) / c->factor;
-            } else {
-                f /= c->factor;
-            }
+    const int pairs = c->rot_dim / 2;
+    double low[8], high = 1.0;
+    for (int i = 0; i < 8; ++i)
+        low[i] = pow(c->theta, -2.0 * i / c->rot_dim);
+    for (int i = 0; i < pairs; ++i) {
+        if (i % 8 == 0)
+            high = pow(c->theta, -2.0 * i / c->rot_dim);
+        double f = high * low[i % 8];
+        if (ramp) {
+            const double r = (double)c->original_len * f / two_pi;
+            double g = (r - c->low_freq) / (c->high_freq - c->low_freq);
+            g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
+            f *= g + (1.0 - g) / c->factor;
+        } else {
+            f /= c->factor;
         }
         t->turns[i] = f / two_pi;
     }
+    for (int i = pairs; i < kRopeMaxPairs; ++i)
+        t->turns[i] = 0.0;
     t->amplitude = (float)c->amplitude;
     return true;
 }
