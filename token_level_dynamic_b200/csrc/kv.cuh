@@ -52,10 +52,13 @@ __device__ __forceinline__ uint2 kv_encode8(const float (&x)[8], uint32_t b)
                 make_float2(x[4 * i + 2] * r, x[4 * i + 3] * r), __NV_SATFINITE, __NV_E4M3);
             w[i] = lo | (hi << 16);
         } else {
-            w[i] = 0;
+            // 1.5 * 2^23 added: the sum's low byte is the product rounded to a whole
+            // number (ties to even), with no conversion instruction
+            uint32_t v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                w[i] |= ((uint32_t)__float2int_rn(x[4 * i + k] * r) & 255u) << (8 * k);
+                v[k] = __float_as_uint(fmaf(x[4 * i + k], r, 12582912.f));
+            w[i] = __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410);
         }
     }
     return b == 255u ? make_uint2(0u, 0u) : make_uint2(w[0], w[1]);

@@ -6,11 +6,12 @@
 // 132 B out per row of an 8-bit cache), at a decoding step's few rows by the
 // launch.  16 lanes hold one row, 8 elements each, so a scale block is 4
 // neighbouring lanes: its largest magnitude takes two shuffles and a row is
-// one coalesced 256-byte access.  With a rotation, K's partners within a pair
+// one coalesced 256-byte access.  A thread has several rows in flight.  With a rotation, K's partners within a pair
 // are in the same lane (interleaved) or, in the half layout, rot_dim / 16
 // lanes away (rot_dim a multiple of 16), so the exchange is a shuffle too and
 // K goes from its bf16 row to its code with one rounding.  A CTA takes whole
-// tokens: their angles are computed once for all heads.
+// tokens of one sequence: their angles are computed once for all heads, and
+// the sequence's length and place are looked up once.
 #include "host.h"
 #include "kv.cuh"
 #include "rope.cuh"
@@ -29,37 +30,46 @@ struct KvArgs {
     const int32_t *start, *count, *pos;
     int64_t tokens, seq_len, cap;     // tokens <= 2^28
     int64_t kt, kh, vt, vh;           // row strides
-    int n_kv, tok_per_cta;
+    int n_kv, tok_per_cta, chunks;    // chunks of a sequence
     int pairs;                        // 0: no rotation
     int inter;
     int32_t *status;
 };
 
-// The cache row of token t (index of its 128-element row for head 0, rows of
-// the next head cap further), or -1: nothing to do.
-__device__ __forceinline__ int64_t kv_slot(const KvArgs &a, int64_t t, int64_t &p)
+// The tokens of a CTA: up to tok_per_cta of one sequence.
+struct KvChunk {
+    int64_t t0, row0;                 // first token; its cache row for head 0 (heads cap rows apart)
+    int nt, start;                    // tokens in range; the first one's position in the cache
+};
+__device__ __forceinline__ KvChunk kv_chunk(const KvArgs &a)
 {
-    const int64_t s = (uint32_t)t / (uint32_t)a.seq_len, i = t - s * a.seq_len;
-    const int64_t n = a.count ? a.count[s] : a.seq_len;
+    const uint32_t s = blockIdx.x / (uint32_t)a.chunks;
+    const int i0 = (int)(blockIdx.x - s * (uint32_t)a.chunks) * a.tok_per_cta;
+    const int n = a.count ? a.count[s] : (int)a.seq_len;
+    const int64_t start = a.start ? a.start[s] : 0;
+    KvChunk c = {};
     if (n < 0 || n > a.seq_len) {
-        set_status(a.status, WIDE_DEV_BAD_RANGE);
-        return -1;
+        if (threadIdx.x == 0)
+            set_status(a.status, WIDE_DEV_BAD_RANGE);
+        return c;
     }
-    if (i >= n)
-        return -1;
-    p = (a.start ? (int64_t)a.start[s] : 0) + i;
-    if (p < 0 || p >= a.cap) {
+    // tokens i0 .. i1 - 1, of which lo .. hi - 1 have a place in the cache
+    const int64_t i1 = min(i0 + a.tok_per_cta, n), lo = max((int64_t)i0, -start), hi = min(i1, a.cap - start);
+    if (i1 > i0 && (lo > i0 || hi < i1) && threadIdx.x == 0)
         set_status(a.status, WIDE_DEV_BAD_RANGE);
-        return -1;
-    }
-    return s * a.n_kv * a.cap + p;
+    c.nt = (int)max(hi - lo, (int64_t)0);
+    c.t0 = s * a.seq_len + lo;
+    c.start = (int)(start + lo);
+    c.row0 = (int64_t)s * a.n_kv * a.cap + c.start;
+    return c;
 }
 
+// One row's 8 elements of this lane into the cache; row < 0: no row (the lane
+// still takes part in its warp's shuffles).
 template <int KIND>
 __device__ __forceinline__ void kv_store_row(void *codes, uint8_t *scales, int64_t row, int l,
                                              const float (&x)[8], const uint4 raw, bool rotated)
 {
-    // row < 0: no row; the lane still takes part in its warp's shuffles
     if constexpr (KIND == WIDE_KV_BF16) {
         if (row < 0)
             return;
@@ -75,146 +85,198 @@ __device__ __forceinline__ void kv_store_row(void *codes, uint8_t *scales, int64
         reinterpret_cast<uint4 *>(codes)[row * (kKvHD / 8) + l] = o;
     } else {
         uint32_t top = 0;             // magnitudes order like their bits, NaN above infinity
+        if (rotated) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+            for (int e = 0; e < 8; ++e)
+                top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+        } else {
+            const uint32_t m = __vmaxu2(__vmaxu2(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu),
+                                        __vmaxu2(raw.z & 0x7fff7fffu, raw.w & 0x7fff7fffu));
+            top = max(m & 0xffff0000u, m << 16);
+        }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const uint32_t b = kv_scale_byte<KIND>(top);
-        const int base = threadIdx.x & 16;
-        uint32_t w = __shfl_sync(0xffffffffu, b, base);
-        w |= __shfl_sync(0xffffffffu, b, base + 4) << 8;
-        w |= __shfl_sync(0xffffffffu, b, base + 8) << 16;
-        w |= __shfl_sync(0xffffffffu, b, base + 12) << 24;
         if (row < 0)
             return;
+        const uint32_t b = kv_scale_byte<KIND>(top);
         reinterpret_cast<uint2 *>(codes)[row * (kKvHD / 8) + l] = kv_encode8<KIND>(x, b);
-        if (l == 0)
-            reinterpret_cast<uint32_t *>(scales)[row] = w;
+        if ((l & 3) == 0)
+            scales[row * (kKvHD / kKvBlock) + (l >> 2)] = (uint8_t)b;
     }
 }
 
-template <int KIND>
+// Rows that a thread of the writer has in flight (the reader: twice as many).
+constexpr int kDeep = 2;
+
+// A thread's rows, 16 apart in the CTA's nt x n_kv (heads fastest), without a
+// division per row.
+struct KvWalk {
+    int i, j;                         // token and head
+    int hop_i, hop_j, n_kv;
+    __device__ __forceinline__ KvWalk(int r, int n) : n_kv(n)
+    {
+        i = r / n;
+        j = r - i * n;
+        hop_i = kRowsAtOnce / n;
+        hop_j = kRowsAtOnce - hop_i * n;
+    }
+    __device__ __forceinline__ void next()
+    {
+        i += hop_i;
+        j += hop_j;
+        if (j >= n_kv) {
+            j -= n_kv;
+            ++i;
+        }
+    }
+};
+
+template <int KIND, bool ROPE>
 __global__ void __launch_bounds__(kThreads)
     kv_append_rows(const __grid_constant__ RopeTable tab, const KvArgs a)
 {
     extern __shared__ float2 cs[];                    // [tok_per_cta][pairs]
-    const int64_t t0 = (int64_t)blockIdx.x * a.tok_per_cta;
-    const int nt = (int)min((int64_t)a.tok_per_cta, a.tokens - t0);
-    if (a.pairs) {
-        for (int i = threadIdx.x; i < nt * a.pairs; i += kThreads) {
+    const KvChunk c = kv_chunk(a);
+    if constexpr (ROPE) {
+        for (int i = threadIdx.x; i < c.nt * a.pairs; i += kThreads) {
             const int t = i / a.pairs, p = i - t * a.pairs;
-            int32_t at;
-            if (a.pos) {
-                at = a.pos[t0 + t];
-            } else {
-                const int64_t s = (uint32_t)(t0 + t) / (uint32_t)a.seq_len;
-                at = (a.start ? a.start[s] : 0) + (int32_t)(t0 + t - s * a.seq_len);
-            }
-            cs[i] = rope_cos_sin(tab.turns[p], at, tab.amplitude);
+            cs[i] = rope_cos_sin(tab.turns[p], a.pos ? a.pos[c.t0 + t] : c.start + t, tab.amplitude);
         }
         __syncthreads();
     }
     const int l = threadIdx.x & 15;
-    const int rows = nt * a.n_kv;
-    for (int r0 = 0; r0 < rows; r0 += kRowsAtOnce) {  // whole warps stay together
-        const int r = r0 + ((int)threadIdx.x >> 4);
-        const int tl = min(r, rows - 1) / a.n_kv, j = min(r, rows - 1) - tl * a.n_kv;
-        const int64_t t = t0 + tl;
-        int64_t p = 0;
-        const int64_t slot = r < rows ? kv_slot(a, t, p) : -1;
-        const int64_t row = slot < 0 ? -1 : slot + j * a.cap;
-        uint4 kw = make_uint4(0u, 0u, 0u, 0u), vw = kw;
-        if (row >= 0) {
-            kw = *reinterpret_cast<const uint4 *>(a.k + t * a.kt + j * a.kh + l * 8);
-            vw = *reinterpret_cast<const uint4 *>(a.v + t * a.vt + j * a.vh + l * 8);
+    const int rows = c.nt * a.n_kv;
+    KvWalk at((int)threadIdx.x >> 4, a.n_kv);
+    for (int r0 = 0; r0 < rows; r0 += kDeep * kRowsAtOnce) {  // whole warps stay together
+        int64_t row[kDeep];
+        int tl[kDeep];
+        uint4 kw[kDeep], vw[kDeep];
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+            const bool in = at.i < c.nt;
+            row[u] = in ? c.row0 + at.j * a.cap + at.i : -1;
+            tl[u] = in ? at.i : 0;
+            kw[u] = vw[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (in) {
+                const int64_t t = c.t0 + at.i;
+                kw[u] = *reinterpret_cast<const uint4 *>(a.k + t * a.kt + at.j * a.kh + l * 8);
+                vw[u] = *reinterpret_cast<const uint4 *>(a.v + t * a.vt + at.j * a.vh + l * 8);
+            }
+            at.next();
         }
-        float x[8];
-        bf16x8_to_f32(kw, x);
-        if (a.pairs) {
-            const float2 *w = cs + tl * a.pairs;
-            if (a.inter) {
-                const int p0 = l * 4;                 // this lane's first pair
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (p0 + i < a.pairs)
-                        rope_pair(x[2 * i], x[2 * i + 1], w[p0 + i]);
-            } else {
-                const int half = a.pairs / 8;         // lanes of the a elements
-                const bool is_a = l < half, is_b = !is_a && l < 2 * half;
-                const int from = (threadIdx.x & 16) + (is_a ? l + half : is_b ? l - half : l);
-                const float2 *wl = w + (is_b ? l - half : is_a ? l : 0) * 8;
+        for (int u = 0; u < kDeep; ++u) {
+            float x[8];
+            bf16x8_to_f32(kw[u], x);
+            if constexpr (ROPE) {
+                const float2 *w = cs + tl[u] * a.pairs;
+                if (a.inter) {
+                    const int p0 = l * 4;             // this lane's first pair
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float y = __shfl_sync(0xffffffffu, x[e], from);
-                    if (is_a)
-                        rope_pair(x[e], y, wl[e]);
-                    else if (is_b)
-                        rope_pair(y, x[e], wl[e]);
+                    for (int i = 0; i < 4; ++i)
+                        if (p0 + i < a.pairs)
+                            rope_pair(x[2 * i], x[2 * i + 1], w[p0 + i]);
+                } else {
+                    const int half = a.pairs / 8;     // lanes of the a elements
+                    const bool is_a = l < half, is_b = !is_a && l < 2 * half;
+                    const int from = (threadIdx.x & 16) + (is_a ? l + half : is_b ? l - half : l);
+                    const float2 *wl = w + (is_b ? l - half : is_a ? l : 0) * 8;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float y = __shfl_sync(0xffffffffu, x[e], from);
+                        if (is_a)
+                            rope_pair(x[e], y, wl[e]);
+                        else if (is_b)
+                            rope_pair(y, x[e], wl[e]);
+                    }
                 }
             }
+            kv_store_row<KIND>(a.kc, a.ks, row[u], l, x, kw[u], ROPE);
+            bf16x8_to_f32(vw[u], x);
+            kv_store_row<KIND>(a.vc, a.vs, row[u], l, x, vw[u], false);
         }
-        kv_store_row<KIND>(a.kc, a.ks, row, l, x, kw, a.pairs != 0);
-        bf16x8_to_f32(vw, x);
-        kv_store_row<KIND>(a.vc, a.vs, row, l, x, vw, false);
     }
 }
 
-template <int KIND>
-__device__ __forceinline__ uint4 kv_load8(const void *codes, const uint8_t *scales, int64_t row,
-                                          int l)
-{
-    if constexpr (KIND == WIDE_KV_BF16) {
-        return reinterpret_cast<const uint4 *>(codes)[row * (kKvHD / 8) + l];
-    } else {
-        const uint2 c = reinterpret_cast<const uint2 *>(codes)[row * (kKvHD / 8) + l];
-        const float s = kv_scale(scales[row * (kKvHD / kKvBlock) + (l >> 2)]);
-        float f[4], g[4];
-        kv_decode4<KIND>(c.x, s, f);
-        kv_decode4<KIND>(c.y, s, g);
-        uint4 o;
-        uint32_t *w = reinterpret_cast<uint32_t *>(&o);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            const __nv_bfloat162 q = __floats2bfloat162_rn(g[2 * i], g[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&p);
-            w[2 + i] = *reinterpret_cast<const uint32_t *>(&q);
+// A lane's 8 elements of a row as they are in the cache.
+template <int KIND> struct KvRaw {
+    uint4 w;                                          // bf16, or codes in x and y
+    uint32_t scale;
+    __device__ __forceinline__ void load(const void *codes, const uint8_t *scales, int64_t row, int l)
+    {
+        if constexpr (KIND == WIDE_KV_BF16) {
+            w = reinterpret_cast<const uint4 *>(codes)[row * (kKvHD / 8) + l];
+        } else {
+            const uint2 c = reinterpret_cast<const uint2 *>(codes)[row * (kKvHD / 8) + l];
+            w.x = c.x;
+            w.y = c.y;
+            scale = scales[row * (kKvHD / kKvBlock) + (l >> 2)];
         }
-        return o;
     }
-}
+    __device__ __forceinline__ uint4 values() const
+    {
+        if constexpr (KIND == WIDE_KV_BF16) {
+            return w;
+        } else {
+            const float s = kv_scale(scale);
+            float f[4], g[4];
+            kv_decode4<KIND>(w.x, s, f);
+            kv_decode4<KIND>(w.y, s, g);
+            uint4 o;
+            uint32_t *q = reinterpret_cast<uint32_t *>(&o);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                const __nv_bfloat162 r = __floats2bfloat162_rn(g[2 * i], g[2 * i + 1]);
+                q[i] = *reinterpret_cast<const uint32_t *>(&p);
+                q[2 + i] = *reinterpret_cast<const uint32_t *>(&r);
+            }
+            return o;
+        }
+    }
+};
 
 template <int KIND> __global__ void __launch_bounds__(kThreads) kv_read_rows(const KvArgs a)
 {
-    const int64_t t0 = (int64_t)blockIdx.x * a.tok_per_cta;
-    const int nt = (int)min((int64_t)a.tok_per_cta, a.tokens - t0);
+    constexpr int kReadDeep = 2 * kDeep;
+    const KvChunk c = kv_chunk(a);
     const int l = threadIdx.x & 15;
-    const int rows = nt * a.n_kv;
-    for (int r = (int)threadIdx.x >> 4; r < rows; r += kRowsAtOnce) {
-        const int tl = r / a.n_kv, j = r - tl * a.n_kv;
-        int64_t p;
-        const int64_t slot = kv_slot(a, t0 + tl, p);
-        if (slot < 0)
-            continue;
-        const int64_t row = slot + j * a.cap, t = t0 + tl;
-        const uint4 kw = kv_load8<KIND>(a.kc, a.ks, row, l);
-        const uint4 vw = kv_load8<KIND>(a.vc, a.vs, row, l);
-        *reinterpret_cast<uint4 *>(a.k_out + t * a.kt + j * a.kh + l * 8) = kw;
-        *reinterpret_cast<uint4 *>(a.v_out + t * a.vt + j * a.vh + l * 8) = vw;
+    KvWalk at((int)threadIdx.x >> 4, a.n_kv);
+    while (at.i < c.nt) {
+        KvRaw<KIND> kw[kReadDeep], vw[kReadDeep];
+        const KvWalk from = at;
+#pragma unroll
+        for (int u = 0; u < kReadDeep; ++u) {
+            if (at.i < c.nt) {
+                const int64_t row = c.row0 + at.j * a.cap + at.i;
+                kw[u].load(a.kc, a.ks, row, l);
+                vw[u].load(a.vc, a.vs, row, l);
+            }
+            at.next();
+        }
+        KvWalk to = from;
+#pragma unroll
+        for (int u = 0; u < kReadDeep; ++u) {
+            if (to.i < c.nt) {
+                const int64_t t = c.t0 + to.i;
+                *reinterpret_cast<uint4 *>(a.k_out + t * a.kt + to.j * a.kh + l * 8) = kw[u].values();
+                *reinterpret_cast<uint4 *>(a.v_out + t * a.vt + to.j * a.vh + l * 8) = vw[u].values();
+            }
+            to.next();
+        }
     }
 }
 
-// Tokens per CTA: about two passes of its 16 row slots, one token at least,
-// while the grid still covers the GPU.
-int kv_tokens_per_cta(int64_t tokens, int n_kv)
+// Tokens per CTA: `deep` passes of its 16 row slots, one token at least, while
+// the grid still covers the GPU.
+void kv_grid(KvArgs *a, int64_t n_seq, int deep)
 {
-    int64_t n = 2 * kRowsAtOnce / n_kv;
-    if (n < 1)
-        n = 1;
-    while (n > 1 && (tokens + n - 1) / n < 296)
+    int64_t n = deep * kRowsAtOnce / a->n_kv;
+    n = n < 1 ? 1 : n > a->seq_len ? a->seq_len : n;
+    while (n > 1 && n_seq * ((a->seq_len + n - 1) / n) < 296)
         n = (n + 1) / 2;
-    return (int)n;
+    a->tok_per_cta = (int)n;
+    a->chunks = (int)((a->seq_len + n - 1) / n);
 }
 
 }  // namespace
@@ -275,7 +337,7 @@ int kv_args(KvArgs *a, const wide_kv_cache *cache, const int32_t *d_start, const
     a->seq_len = r.seq_len;
     a->cap = cache->cap;
     a->n_kv = cache->n_kv;
-    a->tok_per_cta = kv_tokens_per_cta(a->tokens, a->n_kv);
+    kv_grid(a, cache->n_seq, out ? 2 * kDeep : kDeep);
     a->status = status_ptr();
     return WIDE_OK;
 }
@@ -309,15 +371,16 @@ int wide_kv_append(const void *d_k, const void *d_v, const wide_kv_cache *cache,
     a.pairs = rope ? rope->rot_dim / 2 : 0;
     a.inter = rope && rope->layout == WIDE_ROPE_INTERLEAVED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned grid = (unsigned)((a.tokens + a.tok_per_cta - 1) / a.tok_per_cta);
+    const unsigned grid = (unsigned)(cache->n_seq * a.chunks);
     const size_t smem = (size_t)a.tok_per_cta * a.pairs * sizeof(float2);
     LaunchScope scope(KID_KV_APPEND, s);
+    const bool r = a.pairs != 0;
     if (cache->kind == WIDE_KV_BF16)
-        kv_append_rows<WIDE_KV_BF16><<<grid, kThreads, smem, s>>>(tab, a);
+        (r ? kv_append_rows<WIDE_KV_BF16, true> : kv_append_rows<WIDE_KV_BF16, false>)<<<grid, kThreads, smem, s>>>(tab, a);
     else if (cache->kind == WIDE_KV_E4M3)
-        kv_append_rows<WIDE_KV_E4M3><<<grid, kThreads, smem, s>>>(tab, a);
+        (r ? kv_append_rows<WIDE_KV_E4M3, true> : kv_append_rows<WIDE_KV_E4M3, false>)<<<grid, kThreads, smem, s>>>(tab, a);
     else
-        kv_append_rows<WIDE_KV_I8><<<grid, kThreads, smem, s>>>(tab, a);
+        (r ? kv_append_rows<WIDE_KV_I8, true> : kv_append_rows<WIDE_KV_I8, false>)<<<grid, kThreads, smem, s>>>(tab, a);
     return launch_status();
 }
 
@@ -332,7 +395,7 @@ int wide_kv_read(void *d_k, void *d_v, const wide_kv_cache *cache, const int32_t
     a.k_out = static_cast<__nv_bfloat16 *>(d_k);
     a.v_out = static_cast<__nv_bfloat16 *>(d_v);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned grid = (unsigned)((a.tokens + a.tok_per_cta - 1) / a.tok_per_cta);
+    const unsigned grid = (unsigned)(cache->n_seq * a.chunks);
     LaunchScope scope(KID_KV_READ, s);
     if (cache->kind == WIDE_KV_BF16)
         kv_read_rows<WIDE_KV_BF16><<<grid, kThreads, 0, s>>>(a);
