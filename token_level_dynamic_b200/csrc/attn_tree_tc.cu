@@ -18,22 +18,23 @@
 //   MMA      one thread:  S = Q K^T  (M 128 rows, N 128 keys)  and
 //            O += P V  (N 128 dims), fp32 in tensor memory; P, rounded to
 //            bf16, is read from tensor memory too
-//   softmax  two streams of 4 warps.  A row's reference maximum moves only
-//            when it grows by more than 8 (log2 units), to a whole number, so
-//            weights stay within 2^8 and O is rarely rescaled; weights are
-//            computed with the reference so far, and once more if it moves
+//   softmax  8 warps per 128 rows: two threads to a row, each with half of the
+//            keys.  A row's reference maximum moves only when it grows by more
+//            than 8 (log2 units), so weights stay within 2^8 and O is rarely
+//            rescaled: the weights are computed with the reference so far, and
+//            once more if any row of the tile has to move
 //   plan     one warp: the next run and its tokens
-// The two streams have scores, weights and output of their own, so that the
-// MMAs of one run during the softmax of the other: rows 0-127 and 128-255 of a
-// run of more than 128 rows, else the even and the odd tiles of the same rows,
-// whose outputs are added at the end.
+// Runs of at most 128 rows have two tiles of scores and of weights in turn, so
+// the scores of the next keys are ready when a softmax ends.  Larger ones have
+// one per 128 rows, with the weights over the scores' first half, and the two
+// halves' softmax and MMAs overlap each other.
 // Rows along M: a run of at most 64 or 32 rows is repeated R = 2 or 4 times,
-// and a thread takes 128 / R keys of a tile (the weights of a copy for other
-// keys are zero).  The softmax of a thread per row is the longest step with
-// few rows (a warp's exponentials all issue in one quarter of the SM), and
-// this spreads it over the quarters.  The copies are added at the end too.
-// Tensor memory, 512 columns: scores of the streams at 0 and 128, with the
-// weights over their first half; outputs at 256 and 384.
+// and a copy takes 128 / R keys of a tile (its weights for other keys are
+// zero).  The exponentials of a warp all issue in one quarter of the SM, and
+// this spreads those of a few rows over the quarters.  The copies are added at
+// the end.
+// Tensor memory, 512 columns: scores at 0 and 128; output at 256 (and 384 with
+// two halves); weights at 384 and 448.
 #include "attn_tree.cuh"
 #include "host.h"
 #include "kv.cuh"
@@ -55,15 +56,16 @@ template <int KIND, int NM> struct Cfg {
     static constexpr bool k8 = KIND != WIDE_KV_BF16;
     // warps, and registers per thread: every four warps the same number, out of
     // kLaunchRegs each (setmaxnreg); the last of the issuing four idles
-    static constexpr int kSoftWarps = 8, kConvWarps = k8 ? 8 : 4;
+    static constexpr int kSoftWarps = 8 * NM, kConvWarps = k8 ? 8 : 4;
     static constexpr int kMmaWarp = kSoftWarps + kConvWarps, kCopyWarp = kMmaWarp + 1, kPlanWarp = kMmaWarp + 2;
     static constexpr int kWarps = kMmaWarp + 4, kThreads = 32 * kWarps;
-    static constexpr int kLaunchRegs = k8 ? 96 : 128;
-    static constexpr int kConvRegs = 72, kIssueRegs = 64, kSoftRegs = k8 ? 136 : 184;
+    static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+    static constexpr int kConvRegs = NM == 2 ? 48 : 72, kIssueRegs = NM == 2 ? (k8 ? 56 : 48) : 64;
+    static constexpr int kSoftRegs = NM == 2 ? (k8 ? 88 : 96) : k8 ? 136 : 184;
     static_assert(kLaunchRegs * kThreads <= 65536 && kSoftRegs * kSoftWarps + kConvRegs * kConvWarps +
                                                              kIssueRegs * 4 <= kLaunchRegs * kWarps,
                   "registers");
-    static constexpr int kOps = k8 ? 3 : 7 - NM;           // operand tiles
+    static constexpr int kOps = k8 ? 3 : 6 - NM;           // operand tiles
     static constexpr int kRaw = k8 ? 7 - 2 * NM : 1;       // raw tiles (bf16: unused)
     static constexpr uint32_t kOffOps = NM * kTile, kOffRaw = kOffOps + kOps * kTile;
     static constexpr uint32_t kOffScales = kOffRaw + (k8 ? kRaw * kRawCodes : 0);
@@ -79,22 +81,25 @@ struct Run {
     int whole;                   // all of the run's tiles
 };
 
-template <int OPS, int RAW, int ROWS> struct __align__(16) TcCtl {
+template <int OPS, int RAW, int ROWS, int NM> struct __align__(16) TcCtl {
     uint64_t op_full[OPS];                       // bf16: the tile's copies have landed
     uint64_t op_ready[OPS];                      // the convert warps are done with the tile
     uint64_t op_empty[OPS];                      // the MMAs have read it
     uint64_t raw_full[RAW], raw_empty[RAW];      // raw rows landed / converted
     uint64_t q_full;                             // the run's queries are written
-    // of the two streams
+    // of the two tiles in turn, or the two row halves
     uint64_t s_full[2];                          // the scores are complete
-    uint64_t p_full[2];                          // the weights are written (4 warps)
-    uint64_t o_full[2];                          // the run's output is complete
+    uint64_t p_full[2];                          // the weights are written (8 warps)
+    uint64_t pv_done[2];                         // O += P V is complete
+    uint64_t o_full[2];                          // the run's output of a row half is complete
     uint64_t all_done;                           // error path: every MMA is complete
     Run run;                                     // the current one; nt 0: there are no more
     uint32_t tmem;
     int abort, any_bad;
-    int32_t at[ROWS];                            // output row of each row, -1: none
-    int16_t tok[ROWS], list[ROWS];               // its token; tokens of the next run
+    int32_t at[ROWS];                            // output row of each row
+    int16_t tok[ROWS], head[ROWS];               // its token (-1: no row) and query head
+    int16_t list[ROWS];                          // tokens of the next run
+    float pair[2][128 * NM];                     // what the two threads of a row tell each other
     uint32_t bad[kTreeMaxDraft / 32];            // new positions with a value that is not finite
 };
 
@@ -141,21 +146,32 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
-// 32 words of this thread's lane.
-__device__ __forceinline__ void tmem_ld32w(uint32_t taddr, uint32_t *w)
+// 16 fp32 columns of this thread's lane, once they have arrived.
+__device__ __forceinline__ void tmem_get16(uint32_t taddr, float (&v)[16])
 {
-    float v[32];
-    umma::tmem_ld32(taddr, v);
-    tmem_ld_wait_for(v);
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+                   "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                   "+r"(r[13]), "+r"(r[14])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(r[15])::"memory");
 #pragma unroll
-    for (int e = 0; e < 32; ++e)
-        w[e] = __float_as_uint(v[e]);
+    for (int i = 0; i < 16; ++i)
+        v[i] = __uint_as_float(r[i]);
 }
 
 // Weights 2^(sc x - mref) of COLS scores x in tensor memory as bf16 pairs;
 // returns the largest sc x and the sum of the weights.  tail: see(i) has the
-// bits of the scores 32 i .. that the row attends.
-template <int COLS, class See>
+// bits of the scores 32 i .. that the row attends.  CH scores at a time.
+template <int COLS, int CH, class See>
 __device__ __forceinline__ float2 tile_weights(uint32_t ts, float sc, float mref, uint32_t (&pw)[COLS / 2],
                                                bool tail, See &&see)
 {
@@ -164,23 +180,27 @@ __device__ __forceinline__ float2 tile_weights(uint32_t ts, float sc, float mref
     float mx[2] = {-INFINITY, -INFINITY};
     float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-    for (int i = 0; i < COLS / 32; ++i) {
-        float v[32];
-        umma::tmem_ld32(ts + 32 * i, v);
-        tmem_ld_wait_for(v);
+    for (int i = 0; i < COLS / CH; ++i) {
+        float v[CH];
+        if constexpr (CH == 16) {
+            tmem_get16(ts + 16 * i, v);
+        } else {
+            umma::tmem_ld32(ts + 32 * i, v);
+            tmem_ld_wait_for(v);
+        }
         if (tail) {
-            const uint32_t bits = see(i);
+            const uint32_t bits = see(i * CH / 32) >> (i * CH % 32);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
+            for (int e = 0; e < CH; ++e)
                 v[e] = (bits >> e) & 1u ? v[e] : -INFINITY;
         }
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
+        for (int e = 0; e < CH; e += 2) {
             mx[(e >> 1) & 1] = max3(mx[(e >> 1) & 1], v[e], v[e + 1]);
             const float2 x = fma2(make_float2(v[e], v[e + 1]), sc2, mb2);
             const float2 p = make_float2(exp2_sfu(x.x), exp2_sfu(x.y));
             ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], p);
-            pw[i * 16 + e / 2] = pack_bf16(p.x, p.y);
+            pw[(i * CH + e) / 2] = pack_bf16(p.x, p.y);
         }
     }
     ls[0] = add2(ls[0], ls[1]);
@@ -237,14 +257,14 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
-// Barrier of the 8 softmax warps; true if any thread says so.
-__device__ __forceinline__ bool softmax_barrier_or(bool say)
+// Barrier of the 8 softmax warps of row half m; true if any thread says so.
+__device__ __forceinline__ bool softmax_or(int m, bool say)
 {
     uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-                 "barrier.cta.red.or.pred p, 1, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+                 "barrier.cta.red.or.pred p, %1, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(r)
-                 : "r"((uint32_t)say)
+                 : "r"(m + 1), "r"((uint32_t)say)
                  : "memory");
     return r != 0;
 }
@@ -275,6 +295,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *w)
         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]),
         "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
         : "memory");
+}
+
+// As tmem_st16, 8 words.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *w)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 
 // 4 bytes, or zeros if !in (src must still be a valid address).
@@ -372,8 +400,8 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
     using C = Cfg<KIND, NM>;
     constexpr int kThreads = C::kThreads, kMmaWarp = C::kMmaWarp, kCopyWarp = C::kCopyWarp, kPlanWarp = C::kPlanWarp;
     constexpr int rt = NM == 2 ? 256 : 128 / R;       // rows of a run
-    constexpr int kCols = 128 / R;                    // keys of a tile per softmax thread
-    using Ctl = TcCtl<C::kOps, C::kRaw, rt>;
+    constexpr int kMine = 64 / R;                     // keys of a tile per softmax thread
+    using Ctl = TcCtl<C::kOps, C::kRaw, rt, NM>;
     static_assert(C::kOffCtl + sizeof(Ctl) <= 227 * 1024, "shared memory");
     static_assert(128 * (kOPitch * 4 + 8) <= C::kOps * kTile, "a stream's outputs fit in the ring");
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -398,15 +426,9 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
     tree_plan<kThreads>(a, rt, kBK, kRunCost, cum, cnt, reinterpret_cast<uint32_t *>(cnt + kTreeMaxUnits + 2));
     const uint32_t total = cum[U];
     const int n_cta = tree_ctas((int)gridDim.x, total, rt);
-    if (me >= n_cta) {
-        if (tid == 0)
-            a.joins[me] = make_int4(0, 0, 0, 0);
-        if (warp < C::kSoftWarps)
-            tree_zero_skipped<32 * C::kSoftWarps>(a);
-        return;
-    }
-    const uint32_t first = (uint32_t)((uint64_t)me * total / n_cta);
-    const uint32_t end = (uint32_t)((uint64_t)(me + 1) * total / n_cta);
+    // (a CTA past them has no places, and no work but the zeros at the end)
+    const uint32_t first = me < n_cta ? (uint32_t)((uint64_t)me * total / n_cta) : 0u;
+    const uint32_t end = me < n_cta ? (uint32_t)((uint64_t)(me + 1) * total / n_cta) : 0u;
     // of the plan warp: the 32 units from u0 on; lane i holds the places before
     // unit u0 + i + 1, and the tokens of unit u0 + i
     int u0 = 0, mine = 0;
@@ -431,7 +453,8 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
         mbar_init(&ctl->q_full, C::kConvWarps);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->s_full[i], 1);
-            mbar_init(&ctl->p_full[i], 4);
+            mbar_init(&ctl->p_full[i], 8);
+            mbar_init(&ctl->pv_done[i], 1);
             mbar_init(&ctl->o_full[i], 1);
         }
         mbar_init(&ctl->all_done, 1);
@@ -455,10 +478,10 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
     Ring<C::kRaw> raw_at;
     Ring<C::kOps> op_at;
     uint32_t runs = 0;                                // so far
-    // bit m: parity of the tiles of stream m so far, and with it of the
-    // completions of s_full[m] and p_full[m]
+    // bit b: parity of the tiles that scores b have held so far, and with it of
+    // the completions of s_full[b], p_full[b] and pv_done[b]
     uint32_t held = 0;
-    uint32_t o_phase = 0;                             // of this softmax warp's o_full
+    uint32_t o_phase = 0;                             // bit m: parity of the runs of row half m
     bool ok = true;
     int *abort = &ctl->abort;
 
@@ -474,6 +497,7 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
             work();
             held ^= x.nm == 2 ? (nt & 1) * 3u : (((nt + 1) >> 1) & 1u) | ((nt >> 1) & 1u) << 1;
             ++runs;
+            o_phase ^= x.nm == 2 ? 3u : 1u;
             if (__syncthreads_or(!ok))
                 break;
         }
@@ -492,7 +516,7 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
             const int2 len = u < U ? tree_lens(a, s, false) : make_int2(0, 0);
             mine = a.heads ? 0 : len.y;
             if (a.heads)
-#pragma unroll 8
+#pragma unroll 4
                 for (int t = 0; t < len.y; ++t)
                     mine += (a.heads[((size_t)s * a.draft + t) * a.Wh + (j >> 5)] >> (j & 31)) & 1u;
             upto = tree_places(mine * a.rep, rt, (len.x + len.y + kBK - 1) / kBK, kRunCost);
@@ -548,8 +572,13 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
             }
         };
         Run r;
-        bool more = next(r);
-        for (;;) {
+        for (bool current = false;;) {                // a run of which the others work on
+            const bool more = next(r);
+            if (current && __syncthreads_or(0)) {
+                join = make_int4(0, 0, 0, 0);
+                break;
+            }
+            current = more;
             if (lane == 0) {
                 ctl->run = r;
                 ctl->any_bad = 0;
@@ -562,17 +591,13 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                     const int t = (r.run * rt + i) / a.rep, h = r.run * rt + i - t * a.rep;
                     const int tok = i < r.nrows ? ctl->list[t - lo] : -1;
                     ctl->tok[i] = (int16_t)tok;
-                    ctl->at[i] = tok < 0 ? -1 : (r.s * a.draft + tok) * a.n_q + r.j * a.rep + h;
+                    ctl->head[i] = (int16_t)(r.j * a.rep + h);
+                    ctl->at[i] = (r.s * a.draft + tok) * a.n_q + r.j * a.rep + h;
                 }
             }
             __syncthreads();
             if (!more)
                 break;
-            more = next(r);
-            if (__syncthreads_or(0)) {
-                join = make_int4(0, 0, 0, 0);
-                break;
-            }
         }
         if (lane == 0)
             a.joins[me] = join;
@@ -659,22 +684,23 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
         // (8 bits) this thread's row of a tile, its swizzle pattern, and its first block of 32
         const int row = ct & 127, blk = ct >> 7;
         const uint32_t row_swz = swz128(row, 0);
-        // the queries first, 8 loads at a time
+        // the queries first, several loads at a time
+        constexpr int kAtOnce = NM == 2 ? 4 : 8;
+        const __nv_bfloat16 *q_seq = a.q + (int64_t)x.s * a.draft * a.q_stride;
 #pragma unroll 1
-        for (int i0 = ct; i0 < x.nm * 128 * 16; i0 += 8 * kConv) {
-            uint4 w[8];
+        for (int i0 = ct; i0 < x.nm * 128 * 16; i0 += kAtOnce * kConv) {
+            uint4 w[kAtOnce];
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
+            for (int n = 0; n < kAtOnce; ++n) {
                 const int i = i0 + n * kConv, r = i >> 4, c = i & 15;
-                const int q_row = NM == 2 ? r : r & (rt - 1), at = ctl->at[q_row];
+                const int q_row = NM == 2 ? r : r & (rt - 1), tok = ctl->tok[q_row];
                 w[n] = make_uint4(0u, 0u, 0u, 0u);
-                if (at >= 0)
-                    w[n] = *reinterpret_cast<const uint4 *>(
-                        a.q + ((int64_t)x.s * a.draft + ctl->tok[q_row]) * a.q_stride +
-                        (int64_t)(at % a.n_q) * kTreeHD + c * 8);
+                if (tok >= 0)
+                    w[n] = *reinterpret_cast<const uint4 *>(q_seq + (int64_t)tok * a.q_stride +
+                                                            ctl->head[q_row] * kTreeHD + c * 8);
             }
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
+            for (int n = 0; n < kAtOnce; ++n) {
                 const int i = i0 + n * kConv, r = i >> 4, c = i & 15;
                 if (C::k8)                            // dims in the operand order 0 2 1 3
                     w[n] = make_uint4(__byte_perm(w[n].x, w[n].y, 0x5410), __byte_perm(w[n].x, w[n].y, 0x7632),
@@ -769,32 +795,34 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
         auto ready = [&](const Ring<C::kOps> &at) {
             return (C::k8 || wait(&ctl->op_full[at.slot], at.phase)) && wait(&ctl->op_ready[at.slot], at.phase);
         };
-        // S of stream m = rows m * half .. of Q times the tile at `at`; the last to read it frees it
-        auto scores = [&](const Ring<C::kOps> &at, int m, bool last) {
-            const uint64_t q0 = umma::desc_kmajor_sw128(smem_u32(smem) + (two ? (uint32_t)m * kTile : 0u));
+        // scores b = row half m of Q times the tile at `at`; the last to read the tile frees it
+        auto scores = [&](const Ring<C::kOps> &at, int b, int m, bool last) {
+            const uint64_t q0 = umma::desc_kmajor_sw128(smem_u32(smem) + (uint32_t)m * kTile);
             const uint64_t k0 = umma::desc_kmajor_sw128(smem_u32(ops) + at.slot * kTile);
             umma::fence_after_sync();
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kTreeHD / 16; ++k) {
                     const uint32_t off = ((uint32_t)(k >> 2) * kHalf + (uint32_t)(k & 3) * 32u) >> 4;
-                    umma::mma_bf16(tm + (uint32_t)m * 128u, q0 + off, k0 + off, idesc_s, k != 0);
+                    umma::mma_bf16(tm + (uint32_t)b * 128u, q0 + off, k0 + off, idesc_s, k != 0);
                 }
-                umma::commit(&ctl->s_full[m]);
+                umma::commit(&ctl->s_full[b]);
                 if (last)
                     umma::commit(&ctl->op_empty[at.slot]);
             }
             __syncwarp();
         };
-        // O of stream m (+)= P V of the tile at `at`; end: the stream's last
-        auto product = [&](const Ring<C::kOps> &at, int m, bool add, bool last, bool end) {
+        // output of row half m (+)= weights b times the tile at `at`; end: the run's last
+        auto product = [&](const Ring<C::kOps> &at, int b, int m, bool add, bool last, bool end) {
             const uint64_t v0 = umma::desc_mnmajor_sw128(smem_u32(ops) + at.slot * kTile, kHalf);
+            const uint32_t p0 = NM == 2 ? tm + (uint32_t)b * 128u : tm + 384u + (uint32_t)b * 64u;
             umma::fence_after_sync();
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kBK / 16; ++k)
-                    mma_bf16_ta(tm + 256u + (uint32_t)m * 128u, tm + (uint32_t)m * 128u + (uint32_t)k * 8u,
+                    mma_bf16_ta(tm + 256u + (uint32_t)m * 128u, p0 + (uint32_t)k * 8u,
                                 v0 + (uint32_t)k * (16u * 128u >> 4), idesc_pv, add || k != 0);
+                umma::commit(&ctl->pv_done[b]);
                 if (end)
                     umma::commit(&ctl->o_full[m]);
                 if (last)
@@ -802,68 +830,53 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
             }
             __syncwarp();
         };
-        auto weights_ready = [&](int m, int i) {      // of the stream's tile i
-            return wait(&ctl->p_full[m], ((held >> m) + (uint32_t)i) & 1u);
+        auto weights_ready = [&](int b, int i) {      // the i-th of this run in b
+            return wait(&ctl->p_full[b], ((held >> b) + (uint32_t)i) & 1u);
         };
-        // Scores of a stream's next tile come after the product that reads its
-        // weights, which lie over the scores: MMAs complete in order.
-        ok = wait(&ctl->q_full, runs & 1u) && ready(op_at);
+        ok = wait(&ctl->q_full, runs & 1u);
         if (two) {
-            if (ok) {
-                scores(op_at, 0, false);
-                scores(op_at, 1, true);
-                op_at.next();
-            }
+            // scores of a half's next tile come after the product that reads its
+            // weights, which lie over the scores: MMAs complete in order
+            Ring<C::kOps> v_at = op_at;
 #pragma unroll 1
-            for (int t = 0; t < nt && ok; ++t) {
+            for (int t = -1; t < nt && ok; ++t) {
                 const bool more = t + 1 < nt;
-                Ring<C::kOps> k_at = op_at, v_at = op_at;       // K of the next tile, V of this one
+                const Ring<C::kOps> k_at = op_at;               // K of the next tile, then V of this one
                 if (more)
-                    v_at.next();
-                ok = weights_ready(0, t) && ready(v_at);
-                if (!ok)
-                    break;
-                product(v_at, 0, t > 0, false, !more);
-                if (more) {                                     // (complete before V is: the order of use)
-                    ok = ready(k_at);
-                    if (!ok)
-                        break;
-                    scores(k_at, 0, false);
+                    op_at.next();
+#pragma unroll 1
+                for (int m = 0; m < 2 && ok; ++m) {
+                    if (t >= 0) {
+                        ok = weights_ready(m, t) && (m || ready(v_at = op_at));
+                        if (!ok)
+                            break;
+                        product(v_at, m, m, t > 0, m == 1, !more);
+                    }
+                    if (more) {
+                        ok = m || ready(k_at);
+                        if (ok)
+                            scores(k_at, m, m, m == 1);
+                    }
                 }
-                ok = weights_ready(1, t);
-                if (!ok)
-                    break;
-                product(v_at, 1, t > 0, true, !more);
-                if (more)
-                    scores(k_at, 1, true);
-                op_at = v_at;
-                op_at.next();
+                if (t >= 0)
+                    op_at.next();
             }
         } else {
-            // tile t is of stream t & 1:  S(0) S(1)  PV(0) S(2)  PV(1) S(3) ...
-            if (ok) {
-                scores(op_at, 0, true);
-                op_at.next();
-            }
-            if (ok && nt > 1) {
-                ok = ready(op_at);
-                if (ok) {
-                    scores(op_at, 1, true);
-                    op_at.next();
-                }
-            }
+            // S(0)  S(1) PV(0)  S(2) PV(1) ...: scores t + 1 go where the softmax of t - 1 has read
 #pragma unroll 1
-            for (int t = 0; t < nt && ok; ++t) {
-                ok = weights_ready(t & 1, t >> 1) && ready(op_at);
-                if (!ok)
-                    break;
-                product(op_at, t & 1, t > 1, true, t + 2 >= nt);
-                op_at.next();
-                if (t + 2 < nt) {
+            for (int t = -1; t < nt && ok; ++t) {
+                if (t + 1 < nt) {
                     ok = ready(op_at);
                     if (!ok)
                         break;
-                    scores(op_at, t & 1, true);
+                    scores(op_at, (t + 1) & 1, 0, true);
+                    op_at.next();
+                }
+                if (t >= 0) {
+                    ok = weights_ready(t & 1, t >> 1) && ready(op_at);
+                    if (!ok)
+                        break;
+                    product(op_at, t & 1, 0, t > 0, true, t + 1 == nt);
                     op_at.next();
                 }
             }
@@ -882,109 +895,106 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
         // (references: loaded from shared memory where they are used, not held in registers)
         const int &s = x.s, &dl = x.dl, &nrows = x.nrows, &slot = x.slot, &whole = x.whole;
         const int64_t &row0 = x.row0;
-        const int cl = x.cl, blk0 = x.blk0;
+        const int m = NM == 2 ? warp >> 3 : 0, part = (warp >> 2) & 1;    // row half; half of the keys
+        if (m >= x.nm)
+            return;
+        const int cl = x.cl, blk0 = x.blk0, nt = x.nt;
         const bool two = NM == 2 && x.nm == 2;
-        const int m = warp >> 2, quad = warp & 3;             // stream; quarter of its lanes
-        const int r = two ? tid : NM == 2 ? tid & 127 : tid & (rt - 1);   // row of the run
-        const int c0 = R == 1 ? 0 : (tid & 127) / rt * kCols;  // first key of the tile
+        const int quad = warp & 3, tl = 32 * quad + lane;     // this thread's lane of tensor memory
+        const int r = R == 1 ? 128 * m + tl : tl & (rt - 1);  // row of the run
+        const int c0 = tl / (128 / R) * (2 * kMine) + part * kMine;       // first key of the tile
         const uint32_t lanes = (uint32_t)quad << 21;
-        const uint32_t ts = tmem + (uint32_t)m * 128u + lanes, to = ts + 256u;
+        const uint32_t to = tmem + 256u + (uint32_t)m * 128u + lanes;
         const int tok = ctl->tok[r];
         const bool any = (r & ~31) < nrows;                   // a live row in this warp
-        const int n = two ? x.nt : (x.nt + 1 - m) >> 1;       // the stream's tiles
         const float sc = a.scale_log2;
+        float *pair = &ctl->pair[part][128 * m + tl], *other = &ctl->pair[part ^ 1][128 * m + tl];
         float mref = -INFINITY, l = 0.f;
 #pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-            ok = __all_sync(0xffffffffu, tc_wait(&ctl->s_full[m], ((held >> m) + (uint32_t)i) & 1u, abort, a.status));
+        for (int t = 0; t < nt; ++t) {
+            const int b = two ? m : t & 1;
+            ok = __all_sync(0xffffffffu, tc_wait(&ctl->s_full[b], ((held >> b) + (uint32_t)(two ? t : t >> 1)) & 1u,
+                                                 abort, a.status));
+            umma::fence_after_sync();
+            const uint32_t ts = tmem + (uint32_t)b * 128u + lanes;
+            const int k0 = (blk0 + t) * kBK + c0;
+            const auto see = [&](int g) {
+                // (kMine 16: the words are those of 32 keys, from an even multiple of 16 on)
+                return kMine < 32 ? seen_bits(a, s, tok, k0 & ~31, cl, dl) >> (k0 & 31)
+                                  : seen_bits(a, s, tok, k0 + 32 * g, cl, dl);
+            };
+            constexpr int kCh = NM == 2 || kMine < 32 ? 16 : 32;
+            uint32_t pw[kMine / 2];
+            float2 w = make_float2(-INFINITY, 0.f);
+            float alpha = 1.f;
+#pragma unroll 1
+            for (bool again = false;; again = true) {
+                if (any && ok)
+                    w = tile_weights<kMine, kCh>(ts + (uint32_t)c0, sc, mref, pw, k0 + kMine > cl, see);
+                // Every thread of the half says whether its reference has to move (or that it
+                // gives up); it has read its scores then, so weights may be stored over them.
+                if (!softmax_or(m, !ok || (!again && w.x > mref + 8.f)))
+                    break;
+                if (softmax_or(m, !ok)) {
+                    ok = false;
+                    break;
+                }
+                *pair = w.x;
+                softmax_or(m, false);
+                const float top = fmaxf(w.x, *other);
+                if (top > mref + 8.f) {
+                    // a whole number (of log2 units), so that scaling by the step is exact
+                    const float m1 = ceilf(top);
+                    alpha = m1 - mref <= 126.f ? exp2i((int)(mref - m1)) : 0.f;
+                    mref = m1;
+                }
+                if (t > 0) {
+                    // the output so far, half of its columns by each thread of a row
+                    if (!two)                          // (two halves: it came before these scores)
+                        ok = tc_wait(&ctl->pv_done[b ^ 1], ((held >> (b ^ 1)) + (uint32_t)((t - 1) >> 1)) & 1u,
+                                     abort, a.status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    umma::fence_after_sync();
+                    if (ok && __any_sync(0xffffffffu, alpha != 1.f))
+#pragma unroll 1
+                        for (int g = 2 * part; g < 2 * part + 2; ++g) {
+                            float o[32];
+                            umma::tmem_ld32(to + 32 * g, o);
+                            tmem_ld_wait_for(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] *= alpha;
+                            umma::tmem_st32(to + 32 * g, o);
+                        }
+                }
+            }
             if (!ok)
                 break;
-            umma::fence_after_sync();
+            l = l * alpha + w.y;
             if (any) {
-                const int k0 = (blk0 + (two ? i : 2 * i + m)) * kBK + c0;
-                float alpha = 1.f;
-                // up to 64 keys at a time: their weights with the reference maximum so far, and
-                // once more if it moves
-                constexpr int kStep = kCols < 64 ? kCols : 64;
-#pragma unroll 1
-                for (int h = 0; h < kCols / kStep; ++h) {
-                    uint32_t pw[kStep / 2];
-                    float2 w;
-                    float up_by = 1.f;
-                    const int kh = k0 + h * kStep;
-#pragma unroll 1
-                    for (int pass = 0;; ++pass) {
-                        w = tile_weights<kStep>(ts + (uint32_t)(c0 + h * kStep), sc, mref, pw, kh + kStep > cl,
-                                                [&](int g) { return seen_bits(a, s, tok, kh + 32 * g, cl, dl); });
-                        const bool up = w.x > mref + 8.f;
-                        if (pass || !__any_sync(0xffffffffu, up))
-                            break;
-                        if (up) {
-                            // a whole number (of log2 units), so that scaling by the step is exact
-                            const float m1 = ceilf(w.x);
-                            up_by = m1 - mref <= 126.f ? exp2i((int)(mref - m1)) : 0.f;
-                            mref = m1;
-                        }
-                    }
-                    l = l * up_by + w.y;
-                    alpha *= up_by;
-                    if (h && __any_sync(0xffffffffu, up_by != 1.f)) {   // the weights stored before
-                        uint32_t y[32];
-                        umma::tmem_st_wait();
-                        tmem_ld32w(ts, y);
-                        const uint32_t f = pack_bf16(up_by, up_by);
+                const uint32_t tp = (NM == 2 ? ts : tmem + 384u + (uint32_t)b * 64u + lanes) + (uint32_t)(c0 / 2);
+                if constexpr (kMine == 16) {
+                    tmem_st8(tp, pw);
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            y[e] = mul_bf16x2(y[e], f);
-                        tmem_st16(ts, y);
-                        tmem_st16(ts + 16, y + 16);
-                    }
-                    if (R == 1) {
-                        // (over scores that this thread has read: 64 keys take 32 columns)
-#pragma unroll
-                        for (int g = 0; g < kStep / 32; ++g)
-                            tmem_st16(ts + (uint32_t)(h * (kStep / 2) + 16 * g), pw + 16 * g);
-                    } else {
-                        const uint32_t zero[16] = {};
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {         // 32 keys of a tile each
-                            const int k = 32 * g - c0;
-                            if (k == 0)
-                                tmem_st16(ts + 16 * g, pw);
-                            else if (kStep > 32 && k == 32)
-                                tmem_st16(ts + 16 * g, pw + (kStep > 32 ? 16 : 0));
-                            else
-                                tmem_st16(ts + 16 * g, zero);
-                        }
-                    }
-                }
-                if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-                    for (int g = 0; g < 4; ++g) {             // (the product before came before these scores)
-                        float o[32];
-                        umma::tmem_ld32(to + 32 * g, o);
-                        tmem_ld_wait_for(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            o[e] *= alpha;
-                        umma::tmem_st32(to + 32 * g, o);
-                    }
+                    for (int g = 0; g < kMine / 32; ++g)
+                        tmem_st16(tp + 16 * g, pw + 16 * g);
                 }
                 umma::tmem_st_wait();
             }
             umma::fence_before_sync();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&ctl->p_full[m]);
+                mbar_arrive(&ctl->p_full[b]);
         }
-        if (ok && n > 0)
-            ok = __all_sync(0xffffffffu, tc_wait(&ctl->o_full[m], o_phase, abort, a.status));
-        o_phase ^= n > 0 ? 1u : 0u;
-        // both streams here or neither: they meet below
-        if (!two)
-            ok = !softmax_barrier_or(!ok);
+        if (ok)
+            ok = __all_sync(0xffffffffu, tc_wait(&ctl->o_full[m], (o_phase >> m) & 1u, abort, a.status));
+        // the row's sum: both threads' parts
+        *pair = l;
+        ok = !softmax_or(m, !ok);
         if (!ok)
             return;
+        l += *other;
         umma::fence_after_sync();
         // what is not finite in the new positions that the row of token row_tok attends, added
         // to its elements d ..
@@ -1016,99 +1026,57 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                 }
             }
         };
-        auto scale_of = [](float2 ml, float M) {              // of a part to the common maximum M
-            return ml.x > -INFINITY ? exp2f(ml.x - M) : (ml.y == 0.f ? 0.f : 1.f);
-        };
+        const bool live = r < nrows;
+        const int64_t at = max(ctl->at[r], 0);
+        const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
         float *so = reinterpret_cast<float *>(ops);           // the ring, at rest: [128][kOPitch]
         float2 *sml = reinterpret_cast<float2 *>(so + 128 * kOPitch);   // maximum and sum
-        float *mine_o = so + (tid & 127) * kOPitch;
-        float f0 = 1.f, f1 = 0.f;                             // scales of this stream's and the other's output
-        if (!two) {
-            if (m == 1) {
-                if (any && n > 0)
+        if (any)
 #pragma unroll 1
-                    for (int g = 0; g < 4; ++g) {
-                        float o[32];
-                        umma::tmem_ld32(to + 32 * g, o);
-                        tmem_ld_wait_for(o);
+            for (int g = 2 * part; g < 2 * part + 2; ++g) {
+                float o[32];
+                umma::tmem_ld32(to + 32 * g, o);
+                tmem_ld_wait_for(o);
+                if (C::k8)                                    // dims back in order
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(mine_o + 32 * g + e) =
-                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    for (int e = 1; e < 32; e += 4) {
+                        const float y = o[e];
+                        o[e] = o[e + 1];
+                        o[e + 1] = y;
                     }
-                sml[tid & 127] = make_float2(mref, l);
-            }
-            softmax_barrier_or(false);
-            if (m == 0) {
-                const float2 other = sml[tid];
-                const float M = fmaxf(mref, other.x);
-                f0 = scale_of(make_float2(mref, l), M);
-                f1 = scale_of(other, M);
-                l = f0 * l + f1 * other.y;
-                mref = M;
-            }
-        }
-        if (two || m == 0) {
-            const bool live = r < nrows;
-            const int64_t at = max(ctl->at[r], 0);
-            const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-            if (any)
-#pragma unroll 1
-                for (int g = 0; g < 4; ++g) {
-                    float o[32];
-                    umma::tmem_ld32(to + 32 * g, o);
-                    tmem_ld_wait_for(o);
-                    if (!two && x.nt > 1) {                   // (else the other stream has no output)
+                if constexpr (R > 1) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 y = *reinterpret_cast<const float4 *>(mine_o + 32 * g + e);
-                            o[e] = fmaf(f1, y.x, f0 * o[e]);
-                            o[e + 1] = fmaf(f1, y.y, f0 * o[e + 1]);
-                            o[e + 2] = fmaf(f1, y.z, f0 * o[e + 2]);
-                            o[e + 3] = fmaf(f1, y.w, f0 * o[e + 3]);
-                        }
-                    }
-                    if (C::k8)                                // dims back in order
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4 *>(so + tl * kOPitch + 32 * g + e) =
+                            make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                } else if (live) {
+                    add_bad(tok, 32 * g, o);
+                    if (whole) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * kTreeHD + g * 32);
 #pragma unroll
-                        for (int e = 1; e < 32; e += 4) {
-                            const float y = o[e];
-                            o[e] = o[e + 1];
-                            o[e + 1] = y;
-                        }
-                    if constexpr (R > 1) {
+                        for (int e = 0; e < 4; ++e)
+                            dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                                pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                                pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                                pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(a.part_o + ((int64_t)slot * rt + r) * kTreeHD +
+                                                                 g * 32);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(mine_o + 32 * g + e) =
-                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                    } else if (live) {
-                        add_bad(tok, 32 * g, o);
-                        if (whole) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * kTreeHD + g * 32);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                                    pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                                    pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                                    pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-                        } else {
-                            float4 *dst = reinterpret_cast<float4 *>(a.part_o + ((int64_t)slot * rt + r) * kTreeHD +
-                                                                     g * 32);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     }
                 }
-            if constexpr (R > 1) {
-                sml[tid & 127] = make_float2(mref, l);
-            } else if (live && !whole) {
-                a.part_ml[(int64_t)slot * rt + r] = make_float2(mref, l);
-                if (blk0 == 0)
-                    a.join_rows[(int64_t)me * rt + r] = (int32_t)at;
             }
+        if (R == 1 && live && !whole && part == 0) {
+            a.part_ml[(int64_t)slot * rt + r] = make_float2(mref, l);
+            if (blk0 == 0)
+                a.join_rows[(int64_t)me * rt + r] = (int32_t)at;
         }
         if constexpr (R > 1) {                                // add the copies
-            softmax_barrier_or(false);
+            if (part == 0)
+                sml[tl] = make_float2(mref, l);
+            softmax_or(m, false);
 #pragma unroll 1
             for (int row = warp; row < nrows; row += 8) {
                 float M = -INFINITY;
@@ -1120,7 +1088,7 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < R; ++c) {
                     const float2 ml = sml[c * rt + row];
-                    const float f = scale_of(ml, M);
+                    const float f = ml.x > -INFINITY ? exp2f(ml.x - M) : (ml.y == 0.f ? 0.f : 1.f);
                     const float4 y = *reinterpret_cast<const float4 *>(so + (c * rt + row) * kOPitch + lane * 4);
                     L += f * ml.y;
                     acc[0] = fmaf(f, y.x, acc[0]);
@@ -1129,24 +1097,24 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                     acc[3] = fmaf(f, y.w, acc[3]);
                 }
                 add_bad(ctl->tok[row], lane * 4, acc);
-                const int64_t at = ctl->at[row];
+                const int64_t row_at = ctl->at[row];
                 if (whole) {
-                    const float inv = L == 0.f ? 0.f : 1.f / L;
-                    reinterpret_cast<uint2 *>(a.out + at * kTreeHD)[lane] =
-                        make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+                    const float scale = L == 0.f ? 0.f : 1.f / L;
+                    reinterpret_cast<uint2 *>(a.out + row_at * kTreeHD)[lane] =
+                        make_uint2(pack_bf16(acc[0] * scale, acc[1] * scale),
+                                   pack_bf16(acc[2] * scale, acc[3] * scale));
                 } else {
                     reinterpret_cast<float4 *>(a.part_o + ((int64_t)slot * rt + row) * kTreeHD)[lane] =
                         make_float4(acc[0], acc[1], acc[2], acc[3]);
                     if (lane == 0) {
                         a.part_ml[(int64_t)slot * rt + row] = make_float2(M, L);
                         if (blk0 == 0)
-                            a.join_rows[(int64_t)me * rt + row] = (int32_t)at;
+                            a.join_rows[(int64_t)me * rt + row] = (int32_t)row_at;
                     }
                 }
             }
-        }
-        if (!two)
             fence_proxy_async_smem();                         // the ring is written by copies next
+        }
         umma::fence_before_sync();
     };
 
@@ -1168,9 +1136,19 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
         each_run(convert_role);
     } else {
         more_registers<C::kSoftRegs>();
+        if (R > 1) {                                  // the weights of a copy for other copies' keys: zero for good
+            const uint32_t zero[16] = {};
+            if (warp < 4)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    tmem_st16(tmem + 384u + ((uint32_t)warp << 21) + 16 * i, zero);
+            umma::tmem_st_wait();
+            softmax_or(0, false);
+        }
         each_run(softmax_role);
         // zeros of the pairs that are skipped: last, when the CTAs wait for the slowest
-        tree_zero_skipped<32 * C::kSoftWarps>(a);
+        if (warp < 8)
+            tree_zero_skipped<256>(a);
     }
     grid_launch_dependents();
 }
@@ -1180,7 +1158,7 @@ int tiles_launch(const TreeArgs &a, int n, cudaStream_t s)
 {
     using C = Cfg<KIND, NM>;
     constexpr int rt = NM == 2 ? 256 : 128 / R;
-    constexpr size_t smem = C::kOffCtl + sizeof(TcCtl<C::kOps, C::kRaw, rt>);
+    constexpr size_t smem = C::kOffCtl + sizeof(TcCtl<C::kOps, C::kRaw, rt, NM>);
     auto kernel = attn_tree_tiles<KIND, NM, R>;
     CUtensorMap map_k = {}, map_v = {};
     // boxes of 128 rows x 128 bytes: half a bf16 row, or a row of codes (as 64 pairs)
