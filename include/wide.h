@@ -513,7 +513,8 @@ int wide_rope(const void *d_x, const int32_t *d_positions, void *d_out, const wi
  * 8 bits.  An 8-bit cache holds one code per element and one scale per 32
  * elements of a row, uint8 [n_seq][n_kv][cap][head_dim / 32]: a scale byte b
  * stands for 2^(b - 127), and an element's value is code * 2^(b - 127).
- *     WIDE_KV_E4M3   codes are e4m3 numbers, largest 448
+ *     WIDE_KV_E4M3   codes are e4m3 numbers, largest 448 (the NaN codes 7f and
+ *                    ff are never written; what they stand for is not defined)
  *     WIDE_KV_I8     codes are two's complement, -127 .. 127
  * Written: the scale is the smallest power of two s >= 2^-124 with
  * max|x| <= 448 s (127 s), the code is x / s rounded to nearest, ties to
@@ -584,8 +585,10 @@ int wide_kv_read(void *d_k, void *d_v, const wide_kv_cache *cache, const int32_t
  * negative, draft_len > draft or cache_len + draft_len > cap sets
  * WIDE_DEV_BAD_RANGE and is left out.
  * Supported: head_dim 128; n_q a multiple of n_kv, n_q / n_kv <= 32; draft
- * 1 .. 1024; n_seq * n_kv <= 4096.  The work is divided over the GPU on the
- * device from the lengths and masks; results do not depend on timing.
+ * 1 .. 1024; n_seq * n_kv <= 4096; n_seq * n_kv * cap < 2^31.  Up to 16 rows
+ * (draft * n_q / n_kv) run on one kernel, more on another, whose sums are in
+ * another order.  The work is divided over the GPU on the device from the
+ * lengths and masks; results do not depend on timing.
  * Workspace: >= wide_attn_tree_workspace_bytes, 256-byte aligned; contents
  * need not be initialised; calls that share one must be ordered. */
 typedef struct wide_attn_tree_dims {

@@ -119,8 +119,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
             a.joins[me] = make_int4(0, 0, 0, 0);
         return;
     }
-    const uint32_t first = (uint32_t)((uint64_t)me * total / n_cta);
-    const uint32_t end = (uint32_t)((uint64_t)(me + 1) * total / n_cta);
+    const TreeShare share(total, (uint32_t)n_cta);
+    const uint32_t first = share.first(me), end = share.first(me + 1);
     bool joined = false;
     const float sc = a.scale_log2;
 
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
             joined = true;
             if (tid == 0)
                 a.joins[me] = make_int4(
-                    tree_owner(cum[u] + (uint32_t)(run + 1) * per - 1, total, n_cta), slot, nrows, 0);
+                    share.owner(cum[u] + (uint32_t)(run + 1) * per - 1), slot, nrows, 0);
             if (tid < nrows)
                 a.join_rows[me * kRows + tid] = (int32_t)(((int64_t)s * a.draft + stok[tid]) * a.n_q +
                                                           j * a.rep + (run * kRows + tid) % a.rep);
@@ -480,41 +480,71 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
     grid_launch_dependents();
 }
 
-// Adds the parts of the run that starts in CTA blockIdx.x: one warp per row,
-// parts in order.  Few bytes: rows * parts * 512.
+// Adds the parts of the run that starts in CTA blockIdx.x.  Bound by the
+// latency of its few reads (rows * parts * 512 bytes, most of them in L2), so a
+// row's parts are shared out to several warps where there are few rows; always
+// in the same order.
+template <int ROWS> struct JoinCfg {
+    static constexpr int kPer = ROWS >= 256 ? 1 : ROWS >= 128 ? 2 : 4;   // warps of a row
+    static constexpr int kRowsPerBlock = 8 / kPer;
+};
 template <int ROWS>
 __global__ void __launch_bounds__(256)
     attn_tree_join(const float *part_o, const float2 *part_ml, const int4 *joins,
                    const int32_t *join_rows, __nv_bfloat16 *out)
 {
+    using C = JoinCfg<ROWS>;
+    __shared__ float4 sacc[8][32];
     grid_dependency_wait();
-    const int c0 = (int)blockIdx.x;
+    const int c0 = (int)blockIdx.x, lane = threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
     const int4 jn = joins[c0];
-    const int r = (int)blockIdx.y * 8 + ((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (r >= jn.z)
+    const int r0 = (int)blockIdx.y * C::kRowsPerBlock;
+    if (r0 >= jn.z)
         return;
+    const int r = min(r0 + warp / C::kPer, jn.z - 1), sub = warp % C::kPer;
     const int parts = jn.x - c0 + 1;
     // part 0 is in its CTA's second slot, the others in their CTAs' first
+    auto at_of = [&](int i) { return (int64_t)(i ? 2 * (c0 + i) : jn.y) * ROWS + r; };
     float M = -INFINITY;
     for (int i = lane; i < parts; i += 32)
-        M = fmaxf(M, part_ml[(int64_t)(i ? 2 * (c0 + i) : jn.y) * ROWS + r].x);
+        M = fmaxf(M, part_ml[at_of(i)].x);
 #pragma unroll
     for (int off = 16; off; off >>= 1)
         M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    auto scale_of = [&](float2 ml) { return ml.x > -INFINITY ? exp2f(ml.x - M) : (ml.y == 0.f ? 0.f : 1.f); };
     float L = 0.f;
+    for (int i = lane; i < parts; i += 32) {
+        const float2 ml = part_ml[at_of(i)];
+        L += scale_of(ml) * ml.y;
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1)
+        L += __shfl_xor_sync(0xffffffffu, L, off);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-        const int64_t at = (int64_t)(i ? 2 * (c0 + i) : jn.y) * ROWS + r;
-        const float2 ml = part_ml[at];
-        const float4 x = reinterpret_cast<const float4 *>(part_o + at * kTreeHD)[lane];
-        const float f = ml.x > -INFINITY ? exp2f(ml.x - M) : (ml.y == 0.f ? 0.f : 1.f);
-        L += f * ml.y;
+    for (int i = sub; i < parts; i += C::kPer) {
+        const float4 x = reinterpret_cast<const float4 *>(part_o + at_of(i) * kTreeHD)[lane];
+        const float f = scale_of(part_ml[at_of(i)]);
         acc.x = fmaf(f, x.x, acc.x);
         acc.y = fmaf(f, x.y, acc.y);
         acc.z = fmaf(f, x.z, acc.z);
         acc.w = fmaf(f, x.w, acc.w);
     }
+    if constexpr (C::kPer > 1) {
+        sacc[warp][lane] = acc;
+        __syncthreads();
+        if (sub)
+            return;
+        for (int i = 1; i < C::kPer; ++i) {
+            const float4 x = sacc[warp + i][lane];
+            acc.x += x.x;
+            acc.y += x.y;
+            acc.z += x.z;
+            acc.w += x.w;
+        }
+    }
+    if (r0 + warp / C::kPer >= jn.z)
+        return;
     const float inv = L == 0.f ? 0.f : 1.f / L;
     reinterpret_cast<uint2 *>(out + (int64_t)join_rows[c0 * ROWS + r] * kTreeHD)[lane] =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
@@ -563,10 +593,11 @@ int sm_count()
 constexpr int kCtasPerSm = 2;          // of attn_tree_rows
 
 // Which kernel takes the call, by the rows that a unit can have: rows of a run
-// and CTAs.  Up to 16 rows attn_tree_rows, which needs no shared memory for the
-// keys (one token over 2048 keys 20 us and 29 ragged sequences in int8 104 us,
-// against 20 and 106 of attn_tree_tiles); above, its 16 rows a pass read and
-// convert the cache again (16 tokens over 131072 keys in e4m3: 354 us against 106).
+// and CTAs.  Up to 16 rows attn_tree_rows, which starts faster (one token over
+// 2048 bf16 keys 14 us, 29 ragged sequences of 5 tokens in int8 108 us, against
+// 18 and 117 of attn_tree_tiles); above, its 16 rows a pass read and convert
+// the cache again (16 tokens over 131072 e4m3 keys: 354 us against 105, 64 tokens
+// over 4 x 32000 int8 keys 1339 against 230).
 struct TreeChoice {
     int rt, n;
 };
@@ -591,6 +622,8 @@ int tree_check(const wide_kv_cache *c, const wide_attn_tree_dims *d)
     if (d->draft > kTreeMaxDraft || d->n_q / c->n_kv > 32 ||
         c->n_seq * c->n_kv > kTreeMaxUnits || d->q_token_stride % 8 != 0 ||
         c->n_seq * d->draft * d->n_q > (1 << 30) ||
+        // a cache row is a 32-bit coordinate of a copy
+        c->n_seq * c->n_kv * c->cap > (int64_t)0x7fffffff ||
         // the work's places are counted in 32 bits
         c->n_seq * c->n_kv * ((rows + kRows - 1) / kRows) * (c->cap / 32 + 3) > (int64_t)0x7fffffff)
         return WIDE_EUNSUPPORTED;
@@ -613,7 +646,7 @@ template <int ROWS> int tree_join_launch(const TreeArgs &a, int n, cudaStream_t 
 {
     // launched while the attention still runs; it waits for it on the device
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)n, ROWS / 8);
+    cfg.gridDim = dim3((unsigned)n, (ROWS + JoinCfg<ROWS>::kRowsPerBlock - 1) / JoinCfg<ROWS>::kRowsPerBlock);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

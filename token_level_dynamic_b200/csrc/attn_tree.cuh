@@ -7,8 +7,8 @@
 // `rt` of those rows over the unit's keys, in blocks of `bk` keys.  A run takes
 // `rc` places for what it costs beside its blocks, then one for each block (two
 // in a run of more than 128 rows).  All runs' places, unit after unit, form one line of `total`, and
-// CTA c of n takes the blocks whose (first) place is in [c total / n, (c + 1) total / n): equal
-// work for any mixture of lengths and masks, without a value read back by the
+// CTA c of n takes the blocks whose (first) place is in its n-th of the line: equal work for
+// any mixture of lengths and masks, without a value read back by the
 // host.  A CTA that holds only a part of a run (at most its first and its last
 // segment) leaves the part's unnormalised output, maximum and sum in one of its
 // two workspace slots, the first if the run began in an earlier CTA; the CTA
@@ -183,11 +183,17 @@ __device__ __forceinline__ int tree_unit(const uint32_t *cum, int U, uint32_t b)
     return lo;
 }
 
-// Owner of place b when n CTAs share `total`.
-__device__ __forceinline__ int tree_owner(uint32_t b, uint32_t total, int n)
-{
-    return (int)((((uint64_t)b + 1) * (uint64_t)n - 1) / total);
-}
+// The line's `total` places shared out to n CTAs: total % n of them get one more.
+struct TreeShare {
+    uint32_t each, more;               // places of a CTA; CTAs with one more
+    __device__ __forceinline__ TreeShare(uint32_t total, uint32_t n) : each(total / n), more(total - n * each) {}
+    __device__ __forceinline__ uint32_t first(uint32_t c) const { return c * each + min(c, more); }
+    __device__ __forceinline__ int owner(uint32_t b) const
+    {
+        const uint32_t head = more * (each + 1);
+        return (int)(b < head ? b / (each + 1) : more + (b - head) / each);
+    }
+};
 
 // Tokens of the unit that keep the group, numbers [from, to) of them, into
 // tok[]; by one whole warp.

@@ -427,8 +427,8 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
     const uint32_t total = cum[U];
     const int n_cta = tree_ctas((int)gridDim.x, total, rt);
     // (a CTA past them has no places, and no work but the zeros at the end)
-    const uint32_t first = me < n_cta ? (uint32_t)((uint64_t)me * total / n_cta) : 0u;
-    const uint32_t end = me < n_cta ? (uint32_t)((uint64_t)(me + 1) * total / n_cta) : 0u;
+    const TreeShare share(total, max(n_cta, 1));
+    const uint32_t first = me < n_cta ? share.first(me) : 0u, end = me < n_cta ? share.first(me + 1) : 0u;
     // of the plan warp: the 32 units from u0 on; lane i holds the places before
     // unit u0 + i + 1, and the tokens of unit u0 + i
     int u0 = 0, mine = 0;
@@ -510,9 +510,10 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
     // current one.
     auto plan_role = [&] {
         uint32_t b = first;
+        int lo = 0;                                   // the next run's first token among those that keep the group
         int4 join = make_int4(0, 0, 0, 0);
         auto window = [&] {                           // of the 32 units from u0 on, `base` places before them
-            const int u = u0 + lane, s = min(u, U - 1) / a.n_kv, j = u - s * a.n_kv;
+            const int u = u0 + lane, s = (int)((uint32_t)min(u, U - 1) / (uint32_t)a.n_kv), j = u - s * a.n_kv;
             const int2 len = u < U ? tree_lens(a, s, false) : make_int2(0, 0);
             mine = a.heads ? 0 : len.y;
             if (a.heads)
@@ -541,14 +542,14 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                 }
                 const int i = __popc(past), u = u0 + i;    // upto rises with the lane
                 const uint32_t prev = __shfl_sync(0xffffffffu, upto, max(i - 1, 0)), before = i ? prev : base;
-                r.s = u / a.n_kv;
+                r.s = (int)((uint32_t)u / (uint32_t)a.n_kv);
                 r.j = u - r.s * a.n_kv;
                 const int2 len = tree_lens(a, r.s, false);
                 r.cl = len.x;
                 r.dl = len.y;
                 const int nb = (r.cl + r.dl + kBK - 1) / kBK, per = kRunCost + tree_weight(rt) * nb;
                 const int rows = __shfl_sync(0xffffffffu, mine, i) * a.rep;
-                r.run = min((int)(b - before) / per, (rows - 1) / rt);
+                r.run = min((int)((b - before) / (uint32_t)per), (rows - 1) / rt);
                 const uint32_t run0 = before + (uint32_t)r.run * per;   // the run's first place
                 r.nrows = min(rt, rows - r.run * rt);
                 const int w = tree_weight(r.nrows), pos = (int)(b - run0);
@@ -563,9 +564,10 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                 r.slot = 2 * me + (r.blk0 == 0);
                 r.row0 = (int64_t)u * a.cap;
                 if (!r.whole && r.blk0 == 0)          // the run starts here: record its extent
-                    join = make_int4(tree_owner(run0 + (uint32_t)(kRunCost + w * (nb - 1)), total, n_cta),
+                    join = make_int4(share.owner(run0 + (uint32_t)(kRunCost + w * (nb - 1))),
                                      r.slot, r.nrows, 0);
-                tree_tokens(a, r.s, r.j, r.dl, r.run * rt / a.rep, (r.run * rt + r.nrows - 1) / a.rep + 1,
+                lo = (int)((uint32_t)(r.run * rt) / (uint32_t)a.rep);
+                tree_tokens(a, r.s, r.j, r.dl, lo, (int)((uint32_t)(r.run * rt + r.nrows - 1) / (uint32_t)a.rep) + 1,
                             ctl->list);
                 __syncwarp();
                 return true;
@@ -585,10 +587,9 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
             }
             ctl->bad[lane] = 0;
             if (more) {
-                const int lo = r.run * rt / a.rep;
 #pragma unroll 1
                 for (int i = lane; i < rt; i += 32) {
-                    const int t = (r.run * rt + i) / a.rep, h = r.run * rt + i - t * a.rep;
+                    const int t = (int)((uint32_t)(r.run * rt + i) / (uint32_t)a.rep), h = r.run * rt + i - t * a.rep;
                     const int tok = i < r.nrows ? ctl->list[t - lo] : -1;
                     ctl->tok[i] = (int16_t)tok;
                     ctl->head[i] = (int16_t)(r.j * a.rep + h);
