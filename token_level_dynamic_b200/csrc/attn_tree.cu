@@ -213,15 +213,15 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
                             const uint32_t w = word(t.k[n][i], e);
                             uint32_t b0, b1;
                             if constexpr (KIND == WIDE_KV_E4M3) {
-                                b0 = kv_pair<KIND>(__byte_perm(w, 0u, 0x1000), m);
-                                b1 = kv_pair<KIND>(__byte_perm(w, 0u, 0x3020), m);
+                                b0 = kv_pair<KIND>(__byte_perm(w, 0u, 0x1000), m, a.bias);
+                                b1 = kv_pair<KIND>(__byte_perm(w, 0u, 0x3020), m, a.bias);
                                 if (big) {
                                     b0 = mul_bf16x2(b0, mh);
                                     b1 = mul_bf16x2(b1, mh);
                                 }
                             } else {
-                                b0 = kv_pair<KIND>(__byte_perm(w, 0u, 0x0100), m);
-                                b1 = kv_pair<KIND>(__byte_perm(w, 0u, 0x0302), m);
+                                b0 = kv_pair<KIND>(__byte_perm(w, 0u, 0x0100), m, a.bias);
+                                b1 = kv_pair<KIND>(__byte_perm(w, 0u, 0x0302), m, a.bias);
                             }
                             mma16816(sv[n], qf[4 * i + e], b0, b1);
                         }
@@ -356,9 +356,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
                         const uint32_t sel = KIND == WIDE_KV_E4M3 ? (uint32_t)((4 + q) << 12 | q << 4)
                                                                   : (uint32_t)((4 + q) << 8 | q);
                         uint32_t b0 = kv_pair<KIND>(__byte_perm(word(t.v[n][0][0], e >> 2),
-                                                                word(t.v[n][1][0], e >> 2), sel), m01);
+                                                                word(t.v[n][1][0], e >> 2), sel), m01, a.bias);
                         uint32_t b1 = kv_pair<KIND>(__byte_perm(word(t.v[n][2][0], e >> 2),
-                                                                word(t.v[n][3][0], e >> 2), sel), m23);
+                                                                word(t.v[n][3][0], e >> 2), sel), m23, a.bias);
                         if (big) {
                             b0 = mul_bf16x2(b0, h01);
                             b1 = mul_bf16x2(b1, h23);
@@ -721,6 +721,7 @@ int wide_attn_tree(const void *d_q, const wide_kv_cache *cache, const int32_t *d
     a.cap = cache->cap;
     a.q_stride = d->q_token_stride;
     a.scale_log2 = d->scale * kLog2e;
+    a.bias = kKvBias;
     a.part_o = w.part_o;
     a.part_ml = w.part_ml;
     a.joins = w.joins;
