@@ -14,8 +14,9 @@
 //   O += P V    the order of the output dims over the n index is free too:
 //               lane (g, c) reads 16 bytes of the value rows 2c, 2c + 1,
 //               2c + 8, 2c + 9 and pairs the rows up by byte permutes.
-// 8-bit codes become bf16 in registers, exactly: five integer and half-rate
-// float operations per two elements, the scale's multiplication among them.
+// 8-bit codes become bf16 in registers, exactly: two or three integer and two
+// half-rate float operations per two elements, the scale's multiplication among
+// them.
 #include "attn_tree.cuh"
 #include "host.h"
 #include "kv.cuh"
@@ -167,10 +168,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
                 // 8 elements: two k steps (bf16 order) or half a piece (8-bit order)
                 const int d = C::k8 ? (i >> 1) * 64 + c * 16 + (i & 1) * 8 : i * 32 + c * 8;
                 const uint4 w = tok >= 0 ? *reinterpret_cast<const uint4 *>(qr + d) : zero;
-                qf[2 * i][h] = w.x;
-                qf[2 * i][2 + h] = w.y;
-                qf[2 * i + 1][h] = w.z;
-                qf[2 * i + 1][2 + h] = w.w;
+                // 8 bits: elements 0 2 and 1 3 of each four together, as the codes come
+                qf[2 * i][h] = C::k8 ? __byte_perm(w.x, w.y, 0x5410) : w.x;
+                qf[2 * i][2 + h] = C::k8 ? __byte_perm(w.x, w.y, 0x7632) : w.y;
+                qf[2 * i + 1][h] = C::k8 ? __byte_perm(w.z, w.w, 0x5410) : w.z;
+                qf[2 * i + 1][2 + h] = C::k8 ? __byte_perm(w.z, w.w, 0x7632) : w.w;
             }
         }
         const int tok0 = stok[g], tok1 = stok[g + 8];
@@ -212,16 +214,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
                         for (int e = 0; e < 4; ++e) {
                             const uint32_t w = word(t.k[n][i], e);
                             uint32_t b0, b1;
-                            if constexpr (KIND == WIDE_KV_E4M3) {
-                                b0 = kv_pair<KIND>(__byte_perm(w, 0u, 0x1000), m, a.bias);
-                                b1 = kv_pair<KIND>(__byte_perm(w, 0u, 0x3020), m, a.bias);
-                                if (big) {
-                                    b0 = mul_bf16x2(b0, mh);
-                                    b1 = mul_bf16x2(b1, mh);
-                                }
-                            } else {
-                                b0 = kv_pair<KIND>(__byte_perm(w, 0u, 0x0100), m, a.bias);
-                                b1 = kv_pair<KIND>(__byte_perm(w, 0u, 0x0302), m, a.bias);
+                            kv_pairs_0213<KIND>(w, m, a.opaque, b0, b1);
+                            if (KIND == WIDE_KV_E4M3 && big) {
+                                b0 = mul_bf16x2(b0, mh);
+                                b1 = mul_bf16x2(b1, mh);
                             }
                             mma16816(sv[n], qf[4 * i + e], b0, b1);
                         }
@@ -356,9 +352,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
                         const uint32_t sel = KIND == WIDE_KV_E4M3 ? (uint32_t)((4 + q) << 12 | q << 4)
                                                                   : (uint32_t)((4 + q) << 8 | q);
                         uint32_t b0 = kv_pair<KIND>(__byte_perm(word(t.v[n][0][0], e >> 2),
-                                                                word(t.v[n][1][0], e >> 2), sel), m01, a.bias);
+                                                                word(t.v[n][1][0], e >> 2), sel), m01, a.opaque);
                         uint32_t b1 = kv_pair<KIND>(__byte_perm(word(t.v[n][2][0], e >> 2),
-                                                                word(t.v[n][3][0], e >> 2), sel), m23, a.bias);
+                                                                word(t.v[n][3][0], e >> 2), sel), m23, a.opaque);
                         if (big) {
                             b0 = mul_bf16x2(b0, h01);
                             b1 = mul_bf16x2(b1, h23);
@@ -721,7 +717,7 @@ int wide_attn_tree(const void *d_q, const wide_kv_cache *cache, const int32_t *d
     a.cap = cache->cap;
     a.q_stride = d->q_token_stride;
     a.scale_log2 = d->scale * kLog2e;
-    a.bias = kKvBias;
+    a.opaque = kv_opaque(cache->kind);
     a.part_o = w.part_o;
     a.part_ml = w.part_ml;
     a.joins = w.joins;

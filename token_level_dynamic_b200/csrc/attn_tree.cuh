@@ -35,7 +35,7 @@ struct TreeArgs {
     int n_seq, draft, n_q, n_kv, rep, Wt, Wh;
     int64_t cap, q_stride;
     float scale_log2;
-    uint32_t bias;                     // kKvBias
+    uint32_t opaque;                   // kv_opaque of the cache's kind
     // parts: slot 2 c (a run begun in an earlier CTA than c) and 2 c + 1 (begun in c)
     float *part_o;                     // [2 n][rt][128]
     float2 *part_ml;                   // [2 n][rt] (max in log2 units, sum)

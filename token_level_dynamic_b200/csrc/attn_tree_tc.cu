@@ -350,14 +350,14 @@ __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y,
 // 32 codes with one scale byte as bf16 to 64 bytes of a swizzled operand row;
 // dst: address of the first 16 (the next ones differ in bits 4 and 5).
 template <int KIND>
-__device__ __forceinline__ void convert32(uint32_t dst, const uint4 c0, const uint4 c1, uint32_t sc, uint32_t bias)
+__device__ __forceinline__ void convert32(uint32_t dst, const uint4 c0, const uint4 c1, uint32_t sc, uint32_t opaque)
 {
     const uint32_t m = kv_mult<KIND>(sc) * 0x00010001u;
     uint32_t o[16];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const uint32_t x = word(e < 4 ? c0 : c1, e & 3);
-        kv_pairs_0213<KIND>(x, m, bias, o[2 * e], o[2 * e + 1]);
+        kv_pairs_0213<KIND>(x, m, opaque, o[2 * e], o[2 * e + 1]);
     }
     if (KIND == WIDE_KV_E4M3 && sc > 134u && sc < 255u) {
         const uint32_t mh = kv_mult_high(sc) * 0x00010001u;
@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                     const int bk = blk + n * (kConv / 128);     // pieces 2 bk, 2 bk + 1 of the codes' row
                     const uint32_t f = from ^ (uint32_t)(bk << 5);
                     convert32<KIND>((to ^ (uint32_t)((bk & 1) << 6)) + (uint32_t)(bk >> 1) * kHalf,
-                                    ld_shared16(f), ld_shared16(f ^ 16u), (sb4 >> (8 * bk)) & 255u, a.bias);
+                                    ld_shared16(f), ld_shared16(f ^ 16u), (sb4 >> (8 * bk)) & 255u, a.opaque);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();

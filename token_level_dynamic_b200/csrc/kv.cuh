@@ -119,33 +119,35 @@ __device__ __forceinline__ uint32_t kv_mult_high(uint32_t b)
 
 // Two codes, in the bytes of t that the kind wants (e4m3: the high byte of
 // each half; i8: the low byte; the other byte is ignored), as bf16 times mult.
-// bias: kKvBias, as a value that the compiler does not know: an and-or with two
-// immediate operands is two instructions, with one and a register it is one.
-constexpr uint32_t kKvBias = 0x43004300u;
-template <int KIND> __device__ __forceinline__ uint32_t kv_pair(uint32_t t, uint32_t mult, uint32_t bias)
+// opaque: kv_opaque(kind), as a value that the compiler does not know.  i8: an
+// and-or with two immediate operands is two instructions, with one and a
+// register it is one.  e4m3: a left shift is a product in the other pipe.
+__host__ __device__ constexpr uint32_t kv_opaque(int kind) { return kind == WIDE_KV_E4M3 ? 16u : 0x43004300u; }
+template <int KIND> __device__ __forceinline__ uint32_t kv_pair(uint32_t t, uint32_t mult, uint32_t opaque)
 {
     if constexpr (KIND == WIDE_KV_E4M3) {
         // sign, exponent and mantissa to bf16's places: s eeee mmm -> s 0000eeee mmm0000
         return mul_bf16x2(((t >> 4) & 0x07f007f0u) | (t & 0x80008000u), mult);
     } else {
         // 128 + (x & 127) as bf16, minus 128, or minus 256 if the sign bit is set
-        const uint32_t u = (t & 0x007f007fu) | bias, z = (t & 0x00800080u) | bias;
+        const uint32_t u = (t & 0x007f007fu) | opaque, z = (t & 0x00800080u) | opaque;
         return mul_bf16x2(sub_bf16x2(u, z), mult);
     }
 }
 
 // The four codes of word x as bf16 times mult: bytes 0 and 2 in a, 1 and 3 in
 // b.  Bytes two apart are in the two halves already, so there is no permute:
-// five integer instructions for i8, seven for e4m3.
+// five integer instructions a word.
 template <int KIND>
-__device__ __forceinline__ void kv_pairs_0213(uint32_t x, uint32_t mult, uint32_t bias, uint32_t &a, uint32_t &b)
+__device__ __forceinline__ void kv_pairs_0213(uint32_t x, uint32_t mult, uint32_t opaque, uint32_t &a, uint32_t &b)
 {
     if constexpr (KIND == WIDE_KV_E4M3) {
-        a = mul_bf16x2(((x << 4) & 0x07f007f0u) | ((x << 8) & 0x80008000u), mult);
+        const uint32_t y = x * opaque, z = y * opaque;    // x << 4, x << 8
+        a = mul_bf16x2((y & 0x07f007f0u) | (z & 0x80008000u), mult);
         b = mul_bf16x2(((x >> 4) & 0x07f007f0u) | (x & 0x80008000u), mult);
     } else {
-        a = kv_pair<KIND>(x, mult, bias);
-        b = kv_pair<KIND>(x >> 8, mult, bias);
+        a = kv_pair<KIND>(x, mult, opaque);
+        b = kv_pair<KIND>(x >> 8, mult, opaque);
     }
 }
 
