@@ -585,10 +585,10 @@ int wide_kv_read(void *d_k, void *d_v, const wide_kv_cache *cache, const int32_t
  * negative, draft_len > draft or cache_len + draft_len > cap sets
  * WIDE_DEV_BAD_RANGE and is left out.
  * Supported: head_dim 128; n_q a multiple of n_kv, n_q / n_kv <= 32; draft
- * 1 .. 1024; n_seq * n_kv <= 4096; n_seq * n_kv * cap < 2^31.  Up to 16 rows
- * (draft * n_q / n_kv) run on one kernel, more on another, whose sums are in
- * another order.  The work is divided over the GPU on the device from the
- * lengths and masks; results do not depend on timing.
+ * 1 .. 1024; n_seq * n_kv <= 4096; n_seq * n_kv * cap < 2^31.  Few rows
+ * (draft * n_q / n_kv) or a small cache (by cap) run on one kernel, others on
+ * another, whose sums are in another order.  The work is divided over the GPU on
+ * the device from the lengths and masks; results do not depend on timing.
  * Workspace: >= wide_attn_tree_workspace_bytes, 256-byte aligned; contents
  * need not be initialised; calls that share one must be ordered. */
 typedef struct wide_attn_tree_dims {

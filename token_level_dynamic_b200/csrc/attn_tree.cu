@@ -588,21 +588,29 @@ int sm_count()
 
 constexpr int kCtasPerSm = 2;          // of attn_tree_rows
 
-// Which kernel takes the call, by the rows that a unit can have: rows of a run
-// and CTAs.  Up to 16 rows attn_tree_rows, which starts faster (one token over
-// 2048 bf16 keys 14 us, 29 ragged sequences of 5 tokens in int8 108 us, against
-// 18 and 117 of attn_tree_tiles); above, its 16 rows a pass read and convert
-// the cache again (16 tokens over 131072 e4m3 keys: 354 us against 105, 64 tokens
-// over 4 x 32000 int8 keys 1339 against 230).
+// Which kernel takes the call: rows of a run and CTAs.  attn_tree_rows starts
+// faster, attn_tree_tiles reads and converts the cache once for up to 256 rows.
+// Measured (us; rows kernel against tiles kernel; units x rows x keys):
+//   up to 16 rows: one token over 8 x 2048 bf16 keys 14 against 18, 29 ragged
+//     sequences in int8 84 against 100;
+//   32 rows: 8 x 512 keys 12 against 15, 32 x 2000 20 against 20, 32 x 8000 50
+//     against 36; 64 rows: 32 x 512 18 against 19, 32 x 2000 28 against 25;
+//   128 rows: 32 x 128 16 against 20, 32 x 512 24 against 22; 256 rows: 8 x 512
+//     19 against 29, 32 x 512 37 against 31, 128 x 8000 1227 against 214.
+// So the rows kernel takes up to 16 rows, and where its blocks of 16 rows and
+// 128 keys (with every sequence as long as the cache, the lengths being on the
+// device) are few: up to 256, and 5 more for each row of a run of the other.
 struct TreeChoice {
     int rt, n;
 };
 TreeChoice tree_choice(const wide_kv_cache *c, const wide_attn_tree_dims *d)
 {
     const int64_t rows = d->draft * (d->n_q / c->n_kv);
-    if (rows <= kRows)
+    const int rt = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    const int64_t blocks = c->n_seq * c->n_kv * ((rows + kRows - 1) / kRows) * ((c->cap + 127) / 128);
+    if (rows <= kRows || blocks <= 256 + 5 * rt)
         return {kRows, kCtasPerSm * sm_count()};
-    return {rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256, sm_count()};
+    return {rt, sm_count()};
 }
 
 int tree_check(const wide_kv_cache *c, const wide_attn_tree_dims *d)
