@@ -158,10 +158,8 @@ __device__ void tree_plan(const TreeArgs &a, int rt, int bk, int rc, uint32_t *c
     if (lane == 31)
         part[warp] = inc;
     __syncthreads();
-    uint32_t before = inc - sum;
-#pragma unroll 1
-    for (int w = 0; w < warp; ++w)
-        before += part[w];
+    static_assert(THREADS <= 1024, "a lane for each warp");
+    uint32_t before = inc - sum + __reduce_add_sync(0xffffffffu, lane < warp ? part[lane] : 0u);
 #pragma unroll 1
     for (int i = lo; i < hi; ++i) {
         before += cum[i + 1];

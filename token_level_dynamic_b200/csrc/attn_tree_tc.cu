@@ -210,13 +210,10 @@ __device__ __forceinline__ float2 tile_weights(uint32_t ts, float sc, float mref
 // Position in a ring of N slots.
 template <int N> struct Ring {
     uint32_t slot = 0, phase = 0;
-    __device__ __forceinline__ void next(int by = 1)
+    __device__ __forceinline__ void next()
     {
-        slot += (uint32_t)by;
-        if (slot >= N) {
-            slot -= N;
-            phase ^= 1u;
-        }
+        phase ^= slot == N - 1 ? 1u : 0u;
+        slot = slot == N - 1 ? 0 : slot + 1;
     }
     __device__ __forceinline__ void back()
     {
@@ -225,18 +222,21 @@ template <int N> struct Ring {
     }
 };
 
-// A bounded wait: gives up after kPolls polls (each waits some tens of
-// nanoseconds in the hardware), or when another warp has.
-constexpr uint32_t kPolls = 1u << 25;
+// A bounded wait: gives up after kWaitLimitNs, or when another warp has.  The
+// time is read every 1024 polls only.
 __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int *abort, int32_t *status)
 {
+    uint64_t t0 = 0;
 #pragma unroll 1
-    for (uint32_t n = 0; !mbar_try_wait(bar, parity); ++n) {
-        if ((n & 1023u) != 1023u)
+    for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+        if (n & 1023u)
             continue;
         if (*(volatile int *)abort)
             return false;
-        if (n >= kPolls) {
+        const uint64_t now = globaltimer();
+        if (t0 == 0)
+            t0 = now;
+        if (now - t0 > kWaitLimitNs) {
             set_status(status, WIDE_DEV_TIMEOUT);
             *(volatile int *)abort = 1;
             return false;
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
     constexpr int kMine = 64 / R;                     // keys of a tile per softmax thread
     using Ctl = TcCtl<C::kOps, C::kRaw, rt, NM>;
     static_assert(C::kOffCtl + sizeof(Ctl) <= 227 * 1024, "shared memory");
-    static_assert(128 * (kOPitch * 4 + 8) <= C::kOps * kTile, "a stream's outputs fit in the ring");
+    static_assert(128 * (kOPitch * 4 + 8) <= C::kOps * kTile, "the copies' outputs fit in the ring");
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -418,28 +418,10 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + C::kOffCtl);
     uint8_t *ops = smem + C::kOffOps, *raw = smem + C::kOffRaw;
 
-    // ---- the plan, in the ring of operand tiles
-    uint32_t *cum = reinterpret_cast<uint32_t *>(ops);
-    uint16_t *cnt = reinterpret_cast<uint16_t *>(cum + kTreeMaxUnits + 1);
-    static_assert((kTreeMaxUnits + 1) * 4 + (kTreeMaxUnits + 2) * 2 + C::kWarps * 4 <= C::kOps * kTile,
-                  "the plan fits in the ring");
-    tree_plan<kThreads>(a, rt, kBK, kRunCost, cum, cnt, reinterpret_cast<uint32_t *>(cnt + kTreeMaxUnits + 2));
-    const uint32_t total = cum[U];
-    const int n_cta = tree_ctas((int)gridDim.x, total, rt);
-    // (a CTA past them has no places, and no work but the zeros at the end)
-    const TreeShare share(total, max(n_cta, 1));
-    const uint32_t first = me < n_cta ? share.first(me) : 0u, end = me < n_cta ? share.first(me + 1) : 0u;
-    // of the plan warp: the 32 units from u0 on; lane i holds the places before
-    // unit u0 + i + 1, and the tokens of unit u0 + i
-    int u0 = 0, mine = 0;
-    uint32_t base = 0, upto = 0;
-    if (warp == kPlanWarp) {
-        u0 = tree_unit(cum, U, first);
-        base = cum[u0];
-        upto = cum[min(u0 + lane + 1, U)];
-        mine = u0 + lane < U ? cnt[u0 + lane] : 0;
-    }
-    if (tid == 0) {
+    // (before the plan, whose loads other warps wait for meanwhile)
+    if (tid == 32 * kCopyWarp) {
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
         ctl->abort = 0;
         for (int i = 0; i < C::kOps; ++i) {
             mbar_init(&ctl->op_full[i], 1);
@@ -464,9 +446,27 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
         umma::tmem_alloc(&ctl->tmem, 512);
         umma::tmem_relinquish();
     }
-    if (tid == 32 * kCopyWarp) {
-        tma_prefetch_desc(&map_k);
-        tma_prefetch_desc(&map_v);
+
+    // ---- the plan, in the ring of operand tiles
+    uint32_t *cum = reinterpret_cast<uint32_t *>(ops);
+    uint16_t *cnt = reinterpret_cast<uint16_t *>(cum + kTreeMaxUnits + 1);
+    static_assert((kTreeMaxUnits + 1) * 4 + (kTreeMaxUnits + 2) * 2 + C::kWarps * 4 <= C::kOps * kTile,
+                  "the plan fits in the ring");
+    tree_plan<kThreads>(a, rt, kBK, kRunCost, cum, cnt, reinterpret_cast<uint32_t *>(cnt + kTreeMaxUnits + 2));
+    const uint32_t total = cum[U];
+    const int n_cta = tree_ctas((int)gridDim.x, total, rt);
+    // (a CTA past them has no places, and no work but the zeros at the end)
+    const TreeShare share(total, max(n_cta, 1));
+    const uint32_t first = me < n_cta ? share.first(me) : 0u, end = me < n_cta ? share.first(me + 1) : 0u;
+    // of the plan warp: the 32 units from u0 on; lane i holds the places before
+    // unit u0 + i + 1, and the tokens of unit u0 + i
+    int u0 = 0, mine = 0;
+    uint32_t base = 0, upto = 0;
+    if (warp == kPlanWarp) {
+        u0 = tree_unit(cum, U, first);
+        base = cum[u0];
+        upto = cum[min(u0 + lane + 1, U)];
+        mine = u0 + lane < U ? cnt[u0 + lane] : 0;
     }
     fence_proxy_async_smem();                         // the ring is written by copies next
     umma::fence_before_sync();
