@@ -526,6 +526,19 @@ def _invoke(fn: str, dev: int, stream, *args) -> None:
         raise WideError(fn, rc)
 
 
+def _made(make, shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """A tensor of the call's own on like's device.  It is made on the call's
+    stream: zeros are written there, before the kernel, and its memory is given
+    away only behind the stream's work."""
+    dev = like.get_device()
+    if stream is None or dev < 0 or _stream(stream, dev) == _raw_stream(dev):
+        return make(shape, dtype=dtype, device=like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream, dev), device=dev)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=like.device)
+
+
 def _index(t, name: str, n: int):
     """Device pointer of an int32 vector of n elements (None: NULL)."""
     if t is None:
@@ -546,7 +559,7 @@ def wide_rope(x: torch.Tensor, positions: torch.Tensor, rope: WideRopeConfig,
         raise ValueError(f"x must be [T][heads][head_dim], got {tuple(x.shape)}")
     T, n, hd = shape = x.shape
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        out = _made(torch.empty, shape, x.dtype, x, stream)
     elif out.dtype is not x.dtype or out.shape != shape:
         raise ValueError(f"out must be {x.dtype} {tuple(shape)}")
     xt, xh, xe = x.stride()
@@ -653,9 +666,9 @@ def wide_kv_read(cache: dict, start: torch.Tensor, seq_len: int, count: torch.Te
     T = n_seq * seq_len
     make = torch.empty if count is None else torch.zeros
     if k is None:
-        k = make((T, n_kv, hd), dtype=torch.bfloat16, device=cache["k"].device)
+        k = _made(make, (T, n_kv, hd), torch.bfloat16, cache["k"], stream)
     if v is None:
-        v = make((T, n_kv, hd), dtype=torch.bfloat16, device=cache["k"].device)
+        v = _made(make, (T, n_kv, hd), torch.bfloat16, cache["k"], stream)
     rows = _kv_rows(k, v, T, n_kv, hd, seq_len)
     dev = _device_of("wide_kv_read", k=k, v=v, start=start, count=count)
     _invoke("wide_kv_read", dev, stream, k.data_ptr(), v.data_ptr(), _kv_cache(cache, dev),
@@ -717,12 +730,12 @@ def wide_attn_tree(q: torch.Tensor, cache: dict, cache_len: torch.Tensor,
             masks[i] = _dev_ptr(m, name)
     if out is None:
         make = torch.empty if draft_len is None else torch.zeros
-        out = make(shape, dtype=torch.bfloat16, device=q.device)
+        out = _made(make, shape, torch.bfloat16, q, stream)
     elif out.dtype is not torch.bfloat16 or out.shape != shape:
         raise ValueError(f"out must be bfloat16 {tuple(shape)}")
     need = max(256, _attn_tree_workspace(dev, n_seq, n_kv, c.cap, hd, c.kind, draft, n_q))
     if workspace is None or workspace.nbytes < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _made(torch.empty, need, torch.uint8, q, stream)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     d = WideAttnTreeDims(draft, qt if T > 1 else n_q * hd, n_q,
