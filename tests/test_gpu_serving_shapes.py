@@ -6,8 +6,10 @@ and test_gpu_kv_cache.py."""
 import numpy as np
 import pytest
 
+from oracle import serving
 from tests import test_gpu_kv_cache as kv
 from tests import test_gpu_rope as rope
+from tests._util import from_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -97,7 +99,10 @@ def test_append_and_read_in_chunks(kind, n_seq, seq_len, n_kv):
 @pytest.mark.parametrize("rep,N", [(4, 2), (4, 8), (4, 20), (4, 40)])
 def test_attention_past_2_to_31_bytes(rep, N):
     """The same sequence in a cache of 3 GB of codes a tensor (heads 200 MB
-    apart, the last past 2^31 bytes) and in a small one: the same bits."""
+    apart, the last past 2^31 bytes), in a small one and in one of 2048
+    positions, which more than 16 rows of a group take to the large one's
+    kernel: the same bits in the same kernel, and each within the bound of
+    test_gpu_attn_tree.py."""
     import torch
     import token_level_dynamic_b200 as w
     n_kv, cap, have = 16, 3 << 19, 300
@@ -111,4 +116,16 @@ def test_attention_past_2_to_31_bytes(rep, N):
     for c in (big, small):
         w.wide_kv_append(k, v, c)
     cl = torch.tensor([have], dtype=torch.int32, device="cuda")
-    assert torch.equal(w.wide_attn_tree(q, big, cl), w.wide_attn_tree(q, small, cl))
+    same = w.wide_kv_cache(1, n_kv, 2048, torch.int8)
+    w.wide_kv_append(k, v, same)
+    outs = [w.wide_attn_tree(q, c, cl) for c in (big, same, small)]
+    assert torch.equal(outs[0], outs[1])
+    kd, vd = (from_dev(x).reshape(have + N, n_kv, 128).transpose(1, 0, 2)[None]
+              for x in w.wide_kv_read(small, None, have + N))
+    qd = from_dev(q).reshape(1, N, n_kv * rep, 128)
+    ref, spread, reach = serving.attn_tree(qd, kd, vd, [have], [N], np.tril(np.ones((1, N, N), bool)),
+                                           np.ones((1, N, n_kv), bool), 128 ** -0.5, np.zeros(qd.shape))
+    e = 128 * 2.0 ** -23 * reach[..., None]
+    bound = (2.0 ** -8 + 4 * e + 2.0 ** -20) * spread + 2.0 ** -8 * np.abs(ref)
+    for out in (outs[0], outs[2]):
+        assert np.all(np.abs(from_dev(out).reshape(ref.shape) - ref) <= bound)
