@@ -432,6 +432,18 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
                 acc.w = fmaf(f[w], x.w, acc.w);
             }
             const int tok = stok[r];
+            if constexpr (!C::k8) {
+                if (L > 0.f && tree_any_nan(acc.x, acc.y, acc.z, acc.w)) {
+                    const int from = blk0 * C::kBK, n = min(blk1 * C::kBK, len.x) - from;
+                    float y[4];
+                    tree_not_finite(reinterpret_cast<const __nv_bfloat16 *>(vb + (int64_t)from * C::kRowB) + lane * 4,
+                                    n, y);
+                    acc.x = y[0] != 0.f ? y[0] : acc.x;
+                    acc.y = y[1] != 0.f ? y[1] : acc.y;
+                    acc.z = y[2] != 0.f ? y[2] : acc.z;
+                    acc.w = y[3] != 0.f ? y[3] : acc.w;
+                }
+            }
             if (s_any_bad) {
                 // infinities and NaNs of the new positions this row attends
                 for (int jj = 0; jj < len.y; ++jj) {
@@ -483,9 +495,15 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
 template <int ROWS> struct JoinCfg {
     static constexpr int kPer = ROWS >= 256 ? 1 : ROWS >= 128 ? 2 : 4;   // warps of a row
     static constexpr int kRowsPerBlock = 8 / kPer;
+    // Registers for this many blocks on an SM, 32 and 40.  With the 56 that the
+    // compiler takes for its unrolled loop the calls of 8 trees of 61 in bf16
+    // are 69.2 instead of 68.4 us, of 16 trees of 8 in e4m3 43.7 instead of 42.8,
+    // of 29 ragged ones in int8 83.3 instead of 82.3; one token over 2048 bf16
+    // keys is 10.0 instead of 11.2.
+    static constexpr int kBlocksPerSm = ROWS >= 256 ? 7 : 6;
 };
 template <int ROWS>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, JoinCfg<ROWS>::kBlocksPerSm)
     attn_tree_join(const float *part_o, const float2 *part_ml, const int4 *joins,
                    const int32_t *join_rows, __nv_bfloat16 *out)
 {
@@ -541,6 +559,21 @@ __global__ void __launch_bounds__(256)
     }
     if (r0 + warp / C::kPer >= jn.z)
         return;
+    if (L > 0.f && tree_any_nan(acc.x, acc.y, acc.z, acc.w)) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int i = 0; i < parts; ++i) {
+            const float4 x = reinterpret_cast<const float4 *>(part_o + at_of(i) * kTreeHD)[lane];
+            y.x += tree_inf_or_0(x.x);
+            y.y += tree_inf_or_0(x.y);
+            y.z += tree_inf_or_0(x.z);
+            y.w += tree_inf_or_0(x.w);
+        }
+        acc.x = y.x != 0.f ? y.x : acc.x;
+        acc.y = y.y != 0.f ? y.y : acc.y;
+        acc.z = y.z != 0.f ? y.z : acc.z;
+        acc.w = y.w != 0.f ? y.w : acc.w;
+    }
     const float inv = L == 0.f ? 0.f : 1.f / L;
     reinterpret_cast<uint2 *>(out + (int64_t)join_rows[c0 * ROWS + r] * kTreeHD)[lane] =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));

@@ -225,6 +225,34 @@ __device__ __forceinline__ bool tree_sees(const TreeArgs &a, int s, int t, int j
     return (a.tree[((size_t)s * a.draft + t) * a.Wt + (j >> 5)] >> (j & 31)) & 1u;
 }
 
+// Values that are not finite.  A weight is positive, so an infinity attended
+// makes its element of the output that infinity whatever the weight rounds to,
+// but a product gives 0 * inf = NaN where a weight became 0: one too small for
+// its format, an output scaled down to nothing by a later maximum, a copy of a
+// row that takes other keys.  So where a sum comes out as NaN and the weights'
+// does not, its element is the sum of what is not finite alone: of the context's
+// values, which every row attends, or of the parts' outputs.  That costs a
+// comparison an element of the output; only then are the values read again.
+__device__ __forceinline__ float tree_inf_or_0(float x) { return fabsf(x) <= 3.402823466e38f ? 0.f : x; }
+__device__ __forceinline__ bool tree_any_nan(float x, float y, float z, float w)
+{
+    return !(x == x && y == y && z == z && w == w);
+}
+// The sum of what is not finite among 4 elements (v: those of the first row) of
+// n rows of a bf16 cache; 0 where there is none.
+__device__ __forceinline__ void tree_not_finite(const __nv_bfloat16 *v, int n, float (&sum)[4])
+{
+    sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(v + (int64_t)i * kTreeHD);
+        const float x[4] = {bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            sum[e] += tree_inf_or_0(x[e]);
+    }
+}
+
 // Zeros for the pairs of new token and head group that are skipped; the CTAs
 // share the pairs.
 template <int THREADS> __device__ void tree_zero_skipped(const TreeArgs &a)

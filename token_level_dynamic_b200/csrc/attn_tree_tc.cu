@@ -1027,6 +1027,12 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                 }
             }
         };
+        // (bf16) what is not finite in dims d .. of the run's earlier positions
+        bool lost = false;                                    // elements to be made up for, see tree_not_finite
+        const auto not_finite = [&](int d, float (&y)[4]) {
+            tree_not_finite(static_cast<const __nv_bfloat16 *>(a.v) + (row0 + (int64_t)x.blk0 * kBK) * kTreeHD + d,
+                            min((x.blk0 + x.nt) * kBK, x.cl) - x.blk0 * kBK, y);
+        };
         const bool live = r < nrows;
         const int64_t at = max(ctl->at[r], 0);
         const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
@@ -1052,6 +1058,10 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                             make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 } else if (live) {
                     add_bad(tok, 32 * g, o);
+                    if constexpr (!C::k8)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            lost |= o[e] != o[e];
                     if (whole) {
                         uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * kTreeHD + g * 32);
 #pragma unroll
@@ -1068,6 +1078,24 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                             dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     }
                 }
+            }
+        if (R == 1 && !C::k8 && lost && l > 0.f)
+#pragma unroll 1
+            for (int d = 64 * part; d < 64 * part + 64; d += 4) {
+                float y[4], z[4];
+                not_finite(d, y);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    z[e] = y[e];
+                add_bad(tok, d, z);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (y[e] != 0.f) {
+                        if (whole)
+                            a.out[at * kTreeHD + d + e] = __float2bfloat16_rn(z[e] * inv);
+                        else
+                            a.part_o[((int64_t)slot * rt + r) * kTreeHD + d + e] = z[e];
+                    }
             }
         if (R == 1 && live && !whole && part == 0) {
             a.part_ml[(int64_t)slot * rt + r] = make_float2(mref, l);
@@ -1096,6 +1124,15 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                     acc[1] = fmaf(f, y.y, acc[1]);
                     acc[2] = fmaf(f, y.z, acc[2]);
                     acc[3] = fmaf(f, y.w, acc[3]);
+                }
+                if constexpr (!C::k8) {
+                    if (L > 0.f && tree_any_nan(acc[0], acc[1], acc[2], acc[3])) {
+                        float y[4];
+                        not_finite(lane * 4, y);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[e] = y[e] != 0.f ? y[e] : acc[e];
+                    }
                 }
                 add_bad(ctl->tok[row], lane * 4, acc);
                 const int64_t row_at = ctl->at[row];
