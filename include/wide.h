@@ -521,7 +521,9 @@ int wide_rope(const void *d_x, const int32_t *d_positions, void *d_out, const wi
  * even; a block of zeros has b = 0; a block that holds an infinity or a NaN
  * has b = 255 and zero codes, and reads back as NaN.  Powers of two make the
  * division and every value exact: what wide_kv_read returns in bf16, and what
- * the attention multiplies, is the cached value itself.
+ * the attention multiplies, is the cached value itself.  A cache that a caller
+ * fills may hold any b (255: NaN) with any codes whose values bf16 holds; values
+ * between its smallest numbers are rounded to one of them, by all the same.
  */
 #define WIDE_KV_BF16 0
 #define WIDE_KV_E4M3 1

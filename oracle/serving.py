@@ -80,7 +80,7 @@ def kv_decode(codes, byte, kind):
     else:
         c = codes.astype(np.int64)
         v = np.append(_e4m3_grid(), np.nan)[c & 127] * np.where(c & 128, -1.0, 1.0)
-    s = np.where(byte == 255, np.nan, 2.0 ** (np.maximum(byte, 1).astype(np.float64) - 127.0))
+    s = np.where(byte == 255, np.nan, 2.0 ** (byte.astype(np.float64) - 127.0))
     return (v.reshape(*v.shape[:-1], v.shape[-1] // BLOCK, BLOCK) * s[..., None]).reshape(v.shape)
 
 

@@ -124,6 +124,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
     const uint32_t first = share.first(me), end = share.first(me + 1);
     bool joined = false;
     const float sc = a.scale_log2;
+    // (int8) this lane's scale byte of a key row's first 16-byte piece, in both halves
+    const uint32_t k_sel = 0x4040u + 0x0101u * (uint32_t)(c >> 1);
 
     for (uint32_t b = first; b < end;) {
         const int u = tree_unit(cum, U, b);
@@ -208,7 +210,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint32_t sb = (t.ks[n] >> (16 * i + 8 * (c >> 1))) & 255u;
-                        const uint32_t m = kv_mult<KIND>(sb) * 0x00010001u;
+                        const uint32_t m = KIND == WIDE_KV_I8
+                                               ? kv_mult2<KIND>(__byte_perm(t.ks[n], 0u, k_sel + 0x0202u * i))
+                                               : kv_mult<KIND>(sb) * 0x00010001u;
                         const uint32_t mh = kv_mult_high(sb) * 0x00010001u;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -335,10 +339,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
 #pragma unroll
             for (int n = 0; n < C::kNG; ++n) {
                 if constexpr (C::k8) {
-                    const uint32_t m01 = kv_mult<KIND>(t.vs[n] & 255u) |
-                                         kv_mult<KIND>((t.vs[n] >> 8) & 255u) << 16;
-                    const uint32_t m23 = kv_mult<KIND>((t.vs[n] >> 16) & 255u) |
-                                         kv_mult<KIND>(t.vs[n] >> 24) << 16;
+                    const uint32_t m01 = kv_mult2<KIND>(__byte_perm(t.vs[n], 0u, 0x4140));
+                    const uint32_t m23 = kv_mult2<KIND>(__byte_perm(t.vs[n], 0u, 0x4342));
                     const bool big = KIND == WIDE_KV_E4M3 &&
                                      __any_sync(0xffffffffu, __vmaxu4(t.vs[n], 0x86868686u) != 0x86868686u);
                     const uint32_t h01 = kv_mult_high(t.vs[n] & 255u) |

@@ -1,7 +1,9 @@
 // kv.cuh -- the 8-bit cache format: device helpers shared by the cache
 // writer and reader (kv_cache.cu) and the attention over it.
 //
-// A block of 32 elements has one scale byte b, the scale is 2^(b - 127).
+// A block of 32 elements has one scale byte b, the scale is 2^(b - 127); 255
+// stands for NaN.  The writer uses 3 .. 249 and, for a block of zeros, 0; a
+// caller's own cache may hold any byte, and all kernels take the same number.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -64,10 +66,10 @@ __device__ __forceinline__ uint2 kv_encode8(const float (&x)[8], uint32_t b)
     return b == 255u ? make_uint2(0u, 0u) : make_uint2(w[0], w[1]);
 }
 
-// Multiplier of a block with scale byte b (byte 0 stands for zeros).
+// Multiplier of a block with scale byte b (2^-127 is not a normal number).
 __device__ __forceinline__ float kv_scale(uint32_t b)
 {
-    return b == 255u ? __uint_as_float(0x7fffffffu) : exp2i(max((int)b, 1) - 127);
+    return __uint_as_float(b == 255u ? 0x7fffffffu : max(b << 23, 0x00400000u));
 }
 
 // 4 codes (one word) as fp32 numbers times `scale`.
@@ -105,16 +107,31 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
 
 // Multiplier that turns a code, moved into bf16 bits, into its value.  e4m3:
 // the bits stand for value * 2^-120, so the multiplier is 2^(b - 127 + 120);
-// above 2^127 (b > 134) the rest goes into a second one, kv_mult_high.
+// above 2^127 (b > 134) the rest goes into a second one, kv_mult_high.  i8: it is
+// the scale itself, 2^-127 not a normal number.
 template <int KIND> __device__ __forceinline__ uint32_t kv_mult(uint32_t b)
 {
     if (b == 255u)
         return 0x7fffu;
-    return (KIND == WIDE_KV_E4M3 ? min(b + 120u, 254u) : b) << 7;
+    return KIND == WIDE_KV_E4M3 ? min(b + 120u, 254u) << 7 : max(b << 7, 0x40u);
 }
 __device__ __forceinline__ uint32_t kv_mult_high(uint32_t b)
 {
     return (b > 134u && b < 255u ? b - 7u : 127u) << 7;
+}
+
+// kv_mult of the scale bytes in the two halves of b.  i8: three instructions for
+// both; 255 becomes an infinity, and inf * 0 + inf is NaN.
+template <int KIND> __device__ __forceinline__ uint32_t kv_mult2(uint32_t b)
+{
+    if constexpr (KIND == WIDE_KV_E4M3) {
+        return kv_mult<KIND>(b & 255u) | kv_mult<KIND>(b >> 16) << 16;
+    } else {
+        const uint32_t m = __vmaxu2(b << 7, 0x00400040u);
+        uint32_t d;
+        asm("fma.rn.bf16x2 %0, %1, %2, %1;" : "=r"(d) : "r"(m), "r"(0u));
+        return d;
+    }
 }
 
 // Two codes, in the bytes of t that the kind wants (e4m3: the high byte of
