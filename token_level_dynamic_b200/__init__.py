@@ -534,7 +534,11 @@ def _made(make, shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     if stream is None or dev < 0 or _stream(stream, dev) == _raw_stream(dev):
         return make(shape, dtype=dtype, device=like.device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream, dev), device=dev)
+        handle = _stream(stream, dev)
+        # (0 and 1, cudaStreamLegacy, are no streams of their own: an
+        # ExternalStream of 0 is a new one)
+        stream = torch.cuda.default_stream(dev) if handle in (0, 1) else \
+            torch.cuda.ExternalStream(handle, device=dev)
     with torch.cuda.stream(stream):
         return make(shape, dtype=dtype, device=like.device)
 
