@@ -487,8 +487,9 @@ typedef struct wide_rope_config {
     double factor;         /* > 0 */
     double low_freq, high_freq;   /* ramp: turns, 0 <= low_freq < high_freq */
     int64_t original_len;  /* ramp: the original context, >= 0 */
-    double amplitude;      /* A, > 0 */
+    double amplitude;      /* A, > 0, also as fp32 */
 } wide_rope_config;
+/* A frequency whose angle at position 2^31 is past the doubles is refused too. */
 
 typedef struct wide_rope_dims {
     int64_t tokens;

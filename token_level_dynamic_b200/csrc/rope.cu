@@ -26,7 +26,7 @@ bool rope_table(const wide_rope_config *c, RopeTable *t)
     if (!c || c->rot_dim < 2 || c->rot_dim > 2 * kRopeMaxPairs || (c->rot_dim & 1) ||
         (c->layout != WIDE_ROPE_HALF && c->layout != WIDE_ROPE_INTERLEAVED) ||
         !(c->theta > 0.0) || !isfinite(c->theta) || !(c->factor > 0.0) || !isfinite(c->factor) ||
-        !(c->amplitude > 0.0) || !isfinite(c->amplitude) || c->original_len < 0)
+        !((float)c->amplitude > 0.f) || !isfinite((float)c->amplitude) || c->original_len < 0)
         return false;
     const bool ramp = c->factor != 1.0 && c->original_len > 0;
     if (ramp && (!(c->low_freq >= 0.0) || !(c->high_freq > c->low_freq) || !isfinite(c->high_freq)))
@@ -51,6 +51,8 @@ bool rope_table(const wide_rope_config *c, RopeTable *t)
             f /= c->factor;
         }
         t->turns[i] = f / two_pi;
+        if (!isfinite(t->turns[i] * 2147483648.0))   // at the farthest position
+            return false;
     }
     for (int i = pairs; i < kRopeMaxPairs; ++i)
         t->turns[i] = 0.0;
