@@ -600,7 +600,7 @@ typedef struct wide_attn_tree_dims {
     int64_t draft;           /* new-token slots per sequence */
     int64_t q_token_stride;
     int32_t n_q;
-    float scale;             /* > 0: multiplies q . k (1 / sqrt(128) as a rule) */
+    float scale;             /* > 0: multiplies q . k (1 / sqrt(128) as a rule); <= 2^127 */
 } wide_attn_tree_dims;
 
 size_t wide_attn_tree_workspace_bytes(const wide_kv_cache *cache, const wide_attn_tree_dims *d);

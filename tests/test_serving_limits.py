@@ -25,3 +25,13 @@ def test_rope_parameters_at_the_ends_of_their_range(native, good):  # noqa: F811
     L, cfg = native.lib(), _rope_cfg(native, **good)
     d = native.WideRopeDims(0, 40, 128, 0, 0, 0, 0, 0)
     assert L.wide_rope(None, None, None, ctypes.byref(d), ctypes.byref(cfg), None) == native.WIDE_OK
+
+
+@pytest.mark.parametrize("scale,ok", [(1e-45, True), (2.0 ** 127, True), (2.36e38, False), (3.4e38, False)])
+def test_attention_scales_that_the_kernels_can_hold(native, scale, ok):  # noqa: F811
+    """The kernels multiply by scale * log2(e): an infinity makes NaN of scores of zero."""
+    L, d, c = native.lib(), native.WideAttnTreeDims(8, 4096, 32, scale), _cache(native)
+    assert (L.wide_attn_tree_workspace_bytes(ctypes.byref(c), ctypes.byref(d)) > 0) == ok
+    c = _cache(native, n_seq=0, k=None, v=None, ks=None, vs=None)
+    assert L.wide_attn_tree(None, ctypes.byref(c), None, None, None, None, None, ctypes.byref(d), None, 0,
+                            None) == (native.WIDE_OK if ok else native.WIDE_EINVAL)

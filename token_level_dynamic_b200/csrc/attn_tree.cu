@@ -650,8 +650,9 @@ TreeChoice tree_choice(const wide_kv_cache *c, const wide_attn_tree_dims *d)
 
 int tree_check(const wide_kv_cache *c, const wide_attn_tree_dims *d)
 {
+    // (the kernels multiply by scale * log2(e))
     if (!d || d->draft < 1 || d->n_q <= 0 || d->q_token_stride < 0 || !(d->scale > 0.f) ||
-        !(d->scale < 3.4e38f))
+        !isfinite(d->scale * kLog2e))
         return WIDE_EINVAL;
     if (int rc = kv_cache_check(c))
         return rc;
