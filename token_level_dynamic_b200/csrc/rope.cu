@@ -32,7 +32,7 @@ bool rope_table(const wide_rope_config *c, RopeTable *t)
     if (ramp && (!(c->low_freq >= 0.0) || !(c->high_freq > c->low_freq) || !isfinite(c->high_freq)))
         return false;
     // theta^(-2 i / rot_dim) for i = 8 a + b as a product of two powers: 24
-    // calls of pow instead of 128, off by 3 units of 2^-53
+    // calls of pow instead of 128, off by 3 units of 2^-53 (relative)
     const double two_pi = 6.283185307179586476925286766559;
     const int pairs = c->rot_dim / 2;
     double low[8], high = 1.0;

@@ -5,10 +5,14 @@
 // 2 pi) per position, and passes them as a kernel parameter: at most 128
 // doubles, read through the constant bank.  A kernel then needs one double
 // product and one rounding per angle: pos * turns, minus its nearest
-// integer, is the angle within half a turn, whose cosine and sine in fp32
-// (cospi / sinpi of twice that) are within a few units of 2^-24 at any
-// position: the product's error is 2^-53 * |pos * turns| turns, below 2^-22
-// at position 2^31.
+// integer, is the angle within half a turn, whose cosine and sine are taken in
+// fp32 (cospi / sinpi of twice that).  They are off by at most 4 * 2^-24 (the
+// rounded argument, the functions, the amplitude) and, for an angle of x radians
+// before the reduction, 8 * 2^-53 * |x| (the frequency's two powers and three
+// roundings, the product's; the ramp's g makes it 16).  So they are as good as
+// fp32 holds them up to 2^26 radians: position 2^26 where frequencies are at most
+// 1 (theta >= 1, factor >= 1).  Position 2^31 adds 2^-19, a factor below 1 or a
+// theta below 1 makes angles, and that error, larger.
 #pragma once
 
 #include "common.cuh"
