@@ -289,8 +289,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
                     }
             }
 
-            // ---- running maximum (log2 units), moved only when it grows by
-            // more than 8, so weights stay within 2^8 and rescaling is rare
+            // ---- reference of the weights (log2 units): 8 above the maximum when it
+            // moves, which it does only when the maximum passes it, so rescaling is
+            // rare and no weight is above 1
             float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
             for (int n = 0; n < C::kNT; ++n) {
@@ -301,13 +302,15 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_rows(const TreeArgs a)
             x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
             x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2)) * sc;
             x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2)) * sc;
-            if (__any_sync(0xffffffffu, x0 > m0 + 8.f || x1 > m1 + 8.f)) {
+            if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
                 float a0 = 1.f, a1 = 1.f;
-                if (x0 > m0 + 8.f) {
+                if (x0 > m0) {
+                    x0 += kTreeLag;
                     a0 = exp2f(m0 - x0);
                     m0 = x0;
                 }
-                if (x1 > m1 + 8.f) {
+                if (x1 > m1) {
+                    x1 += kTreeLag;
                     a1 = exp2f(m1 - x1);
                     m1 = x1;
                 }

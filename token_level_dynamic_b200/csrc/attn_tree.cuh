@@ -22,6 +22,7 @@ namespace wide {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTreeHD = 128;
+constexpr float kTreeLag = 8.f;          // log2 units by which a row's reference is set above its maximum
 constexpr int kTreeMaxUnits = 4096;
 constexpr int kTreeMaxDraft = 1024;
 
@@ -38,14 +39,14 @@ struct TreeArgs {
     uint32_t opaque;                   // kv_opaque of the cache's kind
     // parts: slot 2 c (a run begun in an earlier CTA than c) and 2 c + 1 (begun in c)
     float *part_o;                     // [2 n][rt][128]
-    float2 *part_ml;                   // [2 n][rt] (max in log2 units, sum)
+    float2 *part_ml;                   // [2 n][rt] (reference in log2 units, sum)
     int4 *joins;                       // [n]: run starting in CTA c: (last CTA, first slot, rows, 0); rows 0: none
     int32_t *join_rows;                // [n][rt] output row of each row of that run
     int32_t *status;
 };
 
 // 2^x by the SFU (results below the normal range become 0, which a weight in
-// bf16 next to one of at least 2^-8 loses anyway)
+// bf16 next to one of at least 2^-9 loses anyway)
 __device__ __forceinline__ float exp2_sfu(float x)
 {
     float y;

@@ -19,10 +19,10 @@
 //            O += P V  (N 128 dims), fp32 in tensor memory; P, rounded to
 //            bf16, is read from tensor memory too
 //   softmax  8 warps per 128 rows: two threads to a row, each with half of the
-//            keys.  A row's reference maximum moves only when it grows by more
-//            than 8 (log2 units), so weights stay within 2^8 and O is rarely
-//            rescaled: the weights are computed with the reference so far, and
-//            once more if any row of the tile has to move
+//            keys.  A row's reference is set 8 (log2 units) above its maximum and
+//            moves only when the maximum passes it, so no weight is above 1 and O
+//            is rarely rescaled: the weights are computed with the reference so
+//            far, and once more if any row of the tile has to move
 //   plan     one warp: the next run and its tokens
 // Runs of at most 128 rows have two tiles of scores and of weights in turn, so
 // the scores of the next keys are ready when a softmax ends.  Larger ones have
@@ -934,7 +934,7 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                     w = tile_weights<kMine, kCh>(ts + (uint32_t)c0, sc, mref, pw, k0 + kMine > cl, see);
                 // Every thread of the half says whether its reference has to move (or that it
                 // gives up); it has read its scores then, so weights may be stored over them.
-                if (!softmax_or(m, !ok || (!again && w.x > mref + 8.f)))
+                if (!softmax_or(m, !ok || (!again && w.x > mref)))
                     break;
                 if (softmax_or(m, !ok)) {
                     ok = false;
@@ -943,9 +943,9 @@ __global__ void __launch_bounds__(Cfg<KIND, NM>::kThreads, 1)
                 *pair = w.x;
                 softmax_or(m, false);
                 const float top = fmaxf(w.x, *other);
-                if (top > mref + 8.f) {
+                if (top > mref) {
                     // a whole number (of log2 units), so that scaling by the step is exact
-                    const float m1 = ceilf(top);
+                    const float m1 = ceilf(top) + kTreeLag;
                     alpha = m1 - mref <= 126.f ? exp2i((int)(mref - m1)) : 0.f;
                     mref = m1;
                 }
