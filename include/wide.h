@@ -502,11 +502,12 @@ typedef struct wide_rope_dims {
 } wide_rope_dims;
 
 /* d_positions: int32 [tokens], any value.  d_out may be d_x itself with the
- * same strides (in place); other overlaps are not allowed.  Any alignment and
- * stride (strides of d_x >= 0; rows of d_out must not overlap); rows whose
- * addresses, head_dim and rotated part are multiples of 16 bytes take the
- * 16-byte path.  tokens == 0 enqueues nothing; head_dim even,
- * <= 1024; heads * head_dim <= 2^20. */
+ * same strides (in place); other overlaps are not allowed.  Any alignment of
+ * whole elements and any stride (strides of d_x >= 0; rows of d_out must not
+ * overlap); rows whose addresses, strides, head_dim and rotated part are
+ * multiples of 16 bytes take the 16-byte path.  tokens == 0 enqueues nothing;
+ * tokens <= 2^28; head_dim even, <= 1024; heads <= 65535; heads * head_dim <=
+ * 2^20 (others: WIDE_EUNSUPPORTED). */
 int wide_rope(const void *d_x, const int32_t *d_positions, void *d_out, const wide_rope_dims *d,
               const wide_rope_config *rope, void *stream);
 
@@ -552,14 +553,17 @@ typedef struct wide_kv_rows {
  * fp32 before it is rounded, by d_positions[t] (int32; NULL: its cache
  * position); rot_dim <= 128 and, in the half layout, a multiple of 16.  V is
  * never rotated.  A count outside 0 .. seq_len or a position outside
- * 0 .. cap - 1 sets WIDE_DEV_BAD_RANGE; those rows are not written. */
+ * 0 .. cap - 1 sets WIDE_DEV_BAD_RANGE; those rows are not written.
+ * Supported (wide_kv_read too): n_seq <= 2^24; n_kv <= 1024; cap <= 2^30; seq_len
+ * <= 2^24; n_seq * seq_len <= 2^28; rows d_k, d_v 16-byte aligned.  The rows must
+ * not overlap the cache. */
 int wide_kv_append(const void *d_k, const void *d_v, const wide_kv_cache *cache,
                    const int32_t *d_start, const int32_t *d_count, const int32_t *d_positions,
                    const wide_kv_rows *rows, const wide_rope_config *rope, void *stream);
 
 /* The reverse: positions start[s] + i, i < count[s], of the cache into rows
- * d_k, d_v (bf16, strided; exact).  Rows at or past count[s] are left as
- * they were.  Errors as for wide_kv_append. */
+ * d_k, d_v (bf16, strided; exact; the two must not overlap).  Rows at or past
+ * count[s] are left as they were.  Errors as for wide_kv_append. */
 int wide_kv_read(void *d_k, void *d_v, const wide_kv_cache *cache, const int32_t *d_start,
                  const int32_t *d_count, const wide_kv_rows *rows, void *stream);
 
@@ -592,7 +596,9 @@ int wide_kv_read(void *d_k, void *d_v, const wide_kv_cache *cache, const int32_t
  * negative, draft_len > draft or cache_len + draft_len > cap sets
  * WIDE_DEV_BAD_RANGE and is left out.
  * Supported: head_dim 128; n_q a multiple of n_kv, n_q / n_kv <= 32; draft
- * 1 .. 1024; n_seq * n_kv <= 4096; n_seq * n_kv * cap < 2^31.  Few rows
+ * 1 .. 1024; n_seq * n_kv <= 4096; n_seq * n_kv * cap < 2^31;
+ * n_seq * n_kv * ceil(draft * n_q / n_kv / 16) * (cap / 32 + 3) < 2^31.
+ * d_q and d_out 16-byte aligned; d_out must not overlap an input.  Few rows
  * (draft * n_q / n_kv) or a small cache (by cap) run on one kernel, others on
  * another, whose sums are in another order.  The work is divided over the GPU on
  * the device from the lengths and masks; results do not depend on timing.

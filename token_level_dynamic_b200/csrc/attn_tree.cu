@@ -661,11 +661,12 @@ int tree_check(const wide_kv_cache *c, const wide_attn_tree_dims *d)
         return rc;
     if (d->n_q % c->n_kv != 0)
         return WIDE_EINVAL;
+    if (d->draft > kTreeMaxDraft || d->n_q / c->n_kv > kTreeMaxRep ||
+        c->n_seq * c->n_kv > kTreeMaxUnits || d->q_token_stride % 8 != 0)
+        return WIDE_EUNSUPPORTED;
+    static_assert((int64_t)kTreeMaxUnits * kTreeMaxRep * kTreeMaxDraft <= 0x7fffffff, "output rows are counted in 32 bits");
     const int64_t rows = d->draft * (d->n_q / c->n_kv);
-    if (d->draft > kTreeMaxDraft || d->n_q / c->n_kv > 32 ||
-        c->n_seq * c->n_kv > kTreeMaxUnits || d->q_token_stride % 8 != 0 ||
-        c->n_seq * d->draft * d->n_q > (1 << 30) ||
-        // a cache row is a 32-bit coordinate of a copy
+    if (// a cache row is a 32-bit coordinate of a copy
         c->n_seq * c->n_kv * c->cap > (int64_t)0x7fffffff ||
         // the work's places are counted in 32 bits
         c->n_seq * c->n_kv * ((rows + kRows - 1) / kRows) * (c->cap / 32 + 3) > (int64_t)0x7fffffff)

@@ -25,6 +25,7 @@ constexpr int kTreeHD = 128;
 constexpr float kTreeLag = 8.f;          // log2 units by which a row's reference is set above its maximum
 constexpr int kTreeMaxUnits = 4096;
 constexpr int kTreeMaxDraft = 1024;
+constexpr int kTreeMaxRep = 32;          // query heads of a KV head
 
 struct TreeArgs {
     const __nv_bfloat16 *q;            // [T][n_q][128], q_stride apart
