@@ -628,9 +628,10 @@ constexpr int kCtasPerSm = 2;          // of attn_tree_rows
 
 // Which kernel takes the call: rows of a run and CTAs.  attn_tree_rows starts
 // faster, attn_tree_tiles reads and converts the cache once for up to 256 rows.
-// Measured (us; rows kernel against tiles kernel; units x rows x keys):
-//   up to 16 rows: one token over 8 x 2048 bf16 keys 14 against 18, 29 ragged
-//     sequences in int8 84 against 100;
+// Measured (us; rows kernel against tiles kernel; units x keys, bf16; int8 differs
+// by up to 16% and in no choice but that of 64 rows over 32 x 512, where both take 19):
+//   up to 16 rows: one token over 8 x 2048 keys 14 against 18, 29 ragged
+//     sequences in int8 80 against 100;
 //   32 rows: 8 x 512 keys 12 against 15, 32 x 2000 20 against 20, 32 x 8000 50
 //     against 36; 64 rows: 32 x 512 18 against 19, 32 x 2000 28 against 25;
 //   128 rows: 32 x 128 16 against 20, 32 x 512 24 against 22; 256 rows: 8 x 512
