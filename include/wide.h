@@ -585,10 +585,12 @@ int wide_kv_read(void *d_k, void *d_v, const wide_kv_cache *cache, const int32_t
  * the product with v (as in the prefill layer).  A pair whose bit in
  * d_head_mask ([n_seq * draft][ceil(n_kv / 32)]; NULL: all kept; bits at or
  * past n_kv are ignored) is clear gets zeros, and so does a row that attends
- * nothing.  Tokens at or past draft_len[s] are left as they were.  A cached value that
- * is not finite reaches only the rows that attend its position, and all of
- * them: weights are positive, so an infinity stays that infinity whatever its
- * weight rounds to (with one of the other sign or a NaN attended too: NaN).
+ * nothing or only scores of minus infinity.  Scores are resolved up to 2^29 in
+ * magnitude (past 2^30 a weight's exponent may leave fp32's range).  Tokens at or
+ * past draft_len[s] are left as they were.  A cached value that is not finite reaches
+ * only the rows that attend its position, and all of them: weights are positive,
+ * so an infinity stays that infinity whatever its weight rounds to (with one of
+ * the other sign or a NaN attended too: NaN).
  *
  * q: bf16 [n_seq * draft][n_q][128], tokens q_token_stride elements apart
  * (a multiple of 8); out: bf16, contiguous.  d_cache_len, d_draft_len:

@@ -37,3 +37,27 @@ def test_a_late_key_with_a_large_value(n, kind):
     want[64:] = -2.0 ** 112
     got = out.double().cpu().numpy()
     assert np.all(np.abs(got - want) <= (2 * 2.0 ** -8 + 2.0 ** -16) * np.abs(want))
+
+
+@pytest.mark.parametrize("cap", [400, 1 << 17])            # the kernel for few positions, and the other
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("n", [1, 4, 8, 16, 32, 64])
+def test_scores_up_to_2_to_29(n, sign, cap):
+    """Scores of +-2^29 at two keys and, elsewhere, of at least 2^21 less: the
+    output is the mean of the two values (1 and 3) to the weights' rounding and
+    its own, 2^-8 each, and 2^-16 for fp32."""
+    import torch
+    import token_level_dynamic_b200 as w
+    have = 300
+    cache = w.wide_kv_cache(1, 1, cap, torch.bfloat16)
+    top, rest = (2.0 ** 14, 2.0 ** 14 * (1 - 2.0 ** -8)) if sign > 0 else (-2.0 ** 14, -2.0 ** 14 * (1 + 2.0 ** -7))
+    cache["k"][0, 0, :have, 0] = rest
+    for i, at in enumerate((10, 290)):
+        cache["k"][0, 0, at, 0] = top
+        cache["v"][0, 0, at] = 1.0 + 2.0 * i
+    cache["v"][0, 0, 100] = 1e30
+    q = torch.zeros((n, 4, 128), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 2.0 ** 15
+    tree = torch.zeros((n, (n + 31) // 32), dtype=torch.int32, device="cuda")
+    out = w.wide_attn_tree(q, cache, torch.full((1,), have, dtype=torch.int32, device="cuda"), tree_mask=tree, scale=1.0)
+    assert float((out.double() - 2.0).abs().max()) <= 2 * (2 * 2.0 ** -8 + 2.0 ** -16)
